@@ -7,6 +7,7 @@ it has not been built (python delta_rule_linear_02_b200/build.py).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -21,6 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libefla.so")
 LIB_CHECKED_PATH = os.path.join(_PKG, "libefla_checked.so")
 
 EFLA_OK, EFLA_ERR_INVALID_ARG, EFLA_ERR_UNSUPPORTED, EFLA_ERR_CUDA, EFLA_ERR_TIMEOUT, EFLA_ERR_BOUNDS = range(6)
+EFLA_ERR_SLOT, EFLA_ERR_FULL = 6, 7
 EFLA_DTYPE_F32, EFLA_DTYPE_BF16 = 0, 1
 EFLA_RULE_EXACT, EFLA_RULE_EULER = 0, 1     # exact-flow gate, or alpha = beta (the delta rule)
 CHUNK = 64
@@ -90,6 +92,33 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.efla_backward_saved_workspace_bytes.restype = Z
     lib.efla_backward_saved.argtypes = [vp] * 11 + [I] * 7 + [vp, Z, vp, Z, vp]
     lib.efla_backward_saved.restype = I
+    lib.efla_scan_workspace_bytes.argtypes = [I] * 7
+    lib.efla_scan_workspace_bytes.restype = Z
+    lib.efla_scan_fwd.argtypes = [vp] * 6 + [I] * 7 + [vp, Z, vp]
+    lib.efla_scan_fwd.restype = I
+    lib.efla_scan_backward_workspace_bytes.argtypes = [I] * 8
+    lib.efla_scan_backward_workspace_bytes.restype = Z
+    lib.efla_scan_backward.argtypes = [vp] * 9 + [I] * 7 + [vp, Z, vp, Z, vp]
+    lib.efla_scan_backward.restype = I
+    lib.efla_scan_step.argtypes = [vp] * 4 + [I] * 6 + [vp]
+    lib.efla_scan_step.restype = I
+    lib.efla_scan_step_paged.argtypes = [vp, vp, vp, I, I, vp, Z, vp, vp, vp] + [I] * 6 + [vp]
+    lib.efla_scan_step_paged.restype = I
+    lib.efla_recurrent_step_paged.argtypes = [vp] * 6 + [I, I, vp, Z, vp, vp, vp] + [I] * 6 + [vp]
+    lib.efla_recurrent_step_paged.restype = I
+    lib.efla_pages_bytes.argtypes = [I, I]
+    lib.efla_pages_bytes.restype = Z
+    lib.efla_pages_init.argtypes = [vp, Z, I, I, vp]
+    lib.efla_pages_free.argtypes = [vp, I, I, vp, I, vp]
+    lib.efla_pages_compact.argtypes = [vp, I, I, vp, Z, Z, vp]
+    lib.efla_pages_status.argtypes = [vp, I, vp]
+    for f in (lib.efla_pages_fork, lib.efla_pages_copy):
+        f.argtypes = [vp, I, I, vp, Z, Z, vp, vp, I, vp]
+    for f in (lib.efla_pages_write, lib.efla_pages_read):
+        f.argtypes = [vp, I, I, vp, Z, vp, Z, vp, I, vp]
+    for f in (lib.efla_pages_init, lib.efla_pages_free, lib.efla_pages_compact, lib.efla_pages_status,
+              lib.efla_pages_fork, lib.efla_pages_copy, lib.efla_pages_write, lib.efla_pages_read):
+        f.restype = I
     return lib
 
 
@@ -467,6 +496,311 @@ def efla_backward(q, k, v, beta, dO, S0=None, dS_T=None, want_dS0: bool = True, 
     return grads
 
 
-__all__ = ["efla_train_saved_bytes", "efla_chunk_fwd_save", "efla_backward_saved", "efla_chunk_fwd_segmented", "efla_chunk_fwd_varlen", "efla_chunk_fwd_gated", "efla_recurrent_step_gated", "efla_backward", "efla_backward_workspace_bytes", "EFLA_RULE_EXACT", "EFLA_RULE_EULER", "efla_gate", "efla_chunk_fwd", "efla_chunk_fwd_noalloc", "efla_chunk_fwd_workspace_bytes", "efla_recurrent_step",
+# ---------------------------------------------------------------- the per-channel gated recurrence
+def _call(fn, where: str, device: torch.device, stream, *args):
+    """fn(*args, stream) with the tensors' device current; `stream` None: that device's current one."""
+    with torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext():
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        status = fn(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+    if status != EFLA_OK:
+        raise EflaError(status, where)
+
+
+def _tensor(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optional[int]:
+    """The address of a contiguous tensor of this type, device and shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _scan_shape(x: torch.Tensor, g: torch.Tensor, cu_seqlens):
+    """(B, H, T, d, g_width, dtype, offsets or None) of a dense [B,H,T,d] or packed [H,T,d] batch."""
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be one of {list(_DTYPES)}, got {x.dtype}")
+    if cu_seqlens is None:
+        if x.dim() != 4:
+            raise ValueError(f"x must be [B,H,T,d], got {tuple(x.shape)}")
+        B, H, T, d = x.shape
+        cu = None
+    else:
+        if x.dim() != 3:
+            raise ValueError(f"x must be [H,T,d] with cu_seqlens, got {tuple(x.shape)}")
+        H, T, d = x.shape
+        cu = torch.as_tensor(cu_seqlens, dtype=torch.int32, device="cpu").contiguous()
+        B = cu.numel() - 1
+        if B < 1 or cu.dim() != 1:
+            raise ValueError("cu_seqlens must hold B + 1 offsets of at least one sequence")
+    if g.shape != x.shape and g.shape != x.shape[:-1]:
+        raise ValueError(f"g must be {tuple(x.shape)} or {tuple(x.shape[:-1])}, got {tuple(g.shape)}")
+    return B, H, T, d, (d if g.dim() == x.dim() else 1), _DTYPES[x.dtype], cu
+
+
+def efla_scan_workspace_bytes(B, H, T, d, g_width, dtype=torch.bfloat16, packed: bool = False) -> int:
+    return int(lib.efla_scan_workspace_bytes(B, H, T, d, g_width, _DTYPES.get(dtype, -1), int(packed)))
+
+
+def _scan_workspace(n: int, device, where: str):
+    if n == 0:
+        raise EflaError(EFLA_ERR_UNSUPPORTED, where)
+    w = torch.empty(n, dtype=torch.uint8, device=device)
+    w[:4].zero_()
+    return w
+
+
+def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule, keep):
+    B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
+    dev = x.device
+    px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", torch.float32, dev, g.shape)
+    pS0 = _tensor(S0, "S0", torch.float32, dev, (B, H, d))
+    if o is None:
+        o = torch.empty_like(x)
+    if S_T is None and want_state:
+        S_T = torch.empty((B, H, d), device=dev, dtype=torch.float32)
+    if workspace is None:
+        n = lib.efla_scan_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None))
+        workspace = (_scan_workspace(n, dev, "efla_scan_workspace_bytes") if keep or not n else
+                     torch.empty(n, dtype=torch.uint8, device=dev))
+    _call(lib.efla_scan_fwd, "efla_scan_fwd", dev, stream, px, pg, None if cu is None else cu.data_ptr(), pS0,
+          _tensor(o, "o", x.dtype, dev, x.shape), _tensor(S_T, "S_T", torch.float32, dev, (B, H, d)), B, H, T, d, gw,
+          dt, int(rule), _tensor(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)), workspace.numel())
+    return o, S_T, workspace
+
+
+def efla_scan_fwd(x, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspace=None, want_state: bool = True,
+                  stream=None, rule: int = EFLA_RULE_EXACT) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The per-channel gated recurrence h_t = e^g_t h_{t-1} + phi(g_t) x_t, o_t = h_t (EFLA_RULE_EULER: 1 for phi).
+    x [B,H,T,d] float32 or bfloat16; g float32, x's shape or [B,H,T] (one decay per head); S0 [B,H,d] float32 or
+    None.  Packed: cu_seqlens (B + 1 offsets, ints or a CPU int32 tensor) with x [H,T,d], g [H,T,d] or [H,T].
+    Returns (o like x, S_T [B,H,d] float32 or None)."""
+    return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule, False)[:2]
+
+
+def efla_scan_fwd_save(x, g, S0=None, cu_seqlens=None, saved=None, o=None, S_T=None, want_state: bool = True,
+                       stream=None, rule: int = EFLA_RULE_EXACT):
+    """efla_scan_fwd that also returns what efla_scan_backward starts from: (o, S_T or None, saved); `saved` is a
+    uint8 tensor of efla_scan_workspace_bytes."""
+    return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, saved, want_state, stream, rule, True)
+
+
+def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None, want_dS0: bool = True, grads=None,
+                       workspace=None, stream=None, rule: int = EFLA_RULE_EXACT):
+    """Gradients of efla_scan_fwd for the loss sum(dO * o) + sum(dS_T * S_T): (dx, dg, dS0 or None), all float32.
+    dO like x, dS_T [B,H,d] float32 or None; saved: from efla_scan_fwd_save on the same x, g, S0, cu_seqlens and rule
+    (None: computed again).  `grads` may supply the three tensors preallocated (dS0 may be None)."""
+    B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
+    dev, f32 = x.device, torch.float32
+    if grads is None:
+        grads = (torch.empty(x.shape, device=dev, dtype=f32), torch.empty(g.shape, device=dev, dtype=f32),
+                 torch.empty((B, H, d), device=dev, dtype=f32) if want_dS0 else None)
+    if workspace is None:
+        n = lib.efla_scan_backward_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None), int(saved is not None))
+        if n == 0:
+            raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_backward_workspace_bytes")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _call(lib.efla_scan_backward, "efla_scan_backward", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
+          _tensor(g, "g", f32, dev, g.shape), None if cu is None else cu.data_ptr(),
+          _tensor(S0, "S0", f32, dev, (B, H, d)), _tensor(dO, "dO", x.dtype, dev, x.shape),
+          _tensor(dS_T, "dS_T", f32, dev, (B, H, d)), _tensor(grads[0], "dx", f32, dev, x.shape),
+          _tensor(grads[1], "dg", f32, dev, g.shape), _tensor(grads[2], "dS0", f32, dev, (B, H, d)), B, H, T, d, gw, dt,
+          int(rule), None if saved is None else _tensor(saved, "saved", torch.uint8, dev, (saved.numel(),)),
+          0 if saved is None else saved.numel(), _tensor(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)),
+          workspace.numel())
+    return grads
+
+
+def _step_shape(x: torch.Tensor, g: torch.Tensor):
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be one of {list(_DTYPES)}, got {x.dtype}")
+    if x.dim() != 3 or (g.shape != x.shape and g.shape != x.shape[:-1]):
+        raise ValueError(f"x must be [N,H,d] and g [N,H,d] or [N,H], got {tuple(x.shape)} and {tuple(g.shape)}")
+    N, H, d = x.shape
+    return N, H, d, (d if g.dim() == 3 else 1), _DTYPES[x.dtype]
+
+
+def efla_scan_step(x, g, S, o=None, stream=None, rule: int = EFLA_RULE_EXACT) -> torch.Tensor:
+    """One token of efla_scan_fwd's recurrence: x [N,H,d], g float32 [N,H,d] or [N,H]; S [N,H,d] float32 updated in
+    place.  Returns o [N,H,d]."""
+    N, H, d, gw, dt = _step_shape(x, g)
+    dev = x.device
+    if o is None:
+        o = torch.empty_like(x)
+    _call(lib.efla_scan_step, "efla_scan_step", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
+          _tensor(g, "g", torch.float32, dev, g.shape), _tensor(S, "S", torch.float32, dev, x.shape),
+          _tensor(o, "o", x.dtype, dev, x.shape), N, H, d, gw, dt, int(rule))
+    return o
+
+
+# ---------------------------------------------------------------- the state cache
+class EflaPages:
+    """The block of a state cache: which page holds the state of which slot.  `block` is an int32 tensor of
+    efla_pages_bytes / 4 words: 64 of header, the table, the owners, scratch."""
+
+    __slots__ = ("block", "n_pages", "n_slots")
+
+    def __init__(self, block: torch.Tensor, n_pages: int, n_slots: int):
+        need = 64 + 2 * n_slots + 3 * n_pages
+        if n_pages < 1 or n_slots < 1:
+            raise ValueError(f"a cache has at least one page and one slot, got {n_pages} and {n_slots}")
+        if not block.is_cuda or block.dtype != torch.int32 or block.dim() != 1 or not block.is_contiguous() \
+                or block.numel() < need:
+            raise ValueError(f"block must be a contiguous CUDA int32 tensor of at least {need} words")
+        self.block, self.n_pages, self.n_slots = block, n_pages, n_slots
+
+    @property
+    def table(self) -> torch.Tensor:
+        """[n_slots] int32: the slot's page, -1 for none."""
+        return self.block[64:64 + self.n_slots]
+
+    @property
+    def owner(self) -> torch.Tensor:
+        """[n_pages] int32: the page's slot, -1 for a free page."""
+        return self.block[64 + self.n_slots:64 + self.n_slots + self.n_pages]
+
+
+def new_pages(n_pages: int, n_slots: int, device="cuda", stream=None) -> EflaPages:
+    """The block of an empty cache of n_pages pages and n_slots slots."""
+    n = int(lib.efla_pages_bytes(n_pages, n_slots))
+    if n == 0:
+        raise EflaError(EFLA_ERR_INVALID_ARG, "efla_pages_bytes")
+    pages = EflaPages(torch.empty(n // 4, dtype=torch.int32, device=device), n_pages, n_slots)
+    _call(lib.efla_pages_init, "efla_pages_init", pages.block.device, stream, pages.block.data_ptr(), n, n_pages,
+          n_slots)
+    return pages
+
+
+def _pool(pool: torch.Tensor, pages: EflaPages, dtype=None) -> Tuple[int, int, int]:
+    """(address, bytes between pages, bytes of a page's data) of a pool [n_pages, ...]: the pages may lie apart (a
+    layer of a larger pool), each page's data is contiguous."""
+    if not pool.is_cuda or pool.device != pages.block.device:
+        raise ValueError(f"pool must be on {pages.block.device}, got {pool.device}")
+    if dtype is not None and pool.dtype != dtype:
+        raise ValueError(f"pool must be {dtype}, got {pool.dtype}")
+    if pool.dim() < 2 or pool.shape[0] != pages.n_pages or not pool[0].is_contiguous():
+        raise ValueError(f"pool must be [{pages.n_pages}, ...] with contiguous pages, got {tuple(pool.shape)}")
+    es = pool.element_size()
+    data = pool[0].numel() * es
+    return pool.data_ptr(), (pool.stride(0) * es if pages.n_pages > 1 else data), data
+
+
+def _slots(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None) -> Optional[int]:
+    return _tensor(t, name, torch.int32, device, (t.numel() if n is None else n,)) if t is not None else None
+
+
+def efla_pages_fork(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Tensor, stream=None) -> None:
+    """Every empty slot dest[i] gets a free page with a copy of slot source[i]'s page (-1: zeros).  pool [n_pages, ...]
+    (any type), or None: pages are given without copying.  source, dest: int32, -1 in dest is padding."""
+    dev = pages.block.device
+    ptr, stride, data = (None, 0, 0) if pool is None else _pool(pool, pages)
+    _call(lib.efla_pages_fork, "efla_pages_fork", dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr,
+          stride, data, _slots(source, "source", dev, dest.numel()), _slots(dest, "dest", dev), dest.numel())
+
+
+def efla_pages_copy(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Tensor, stream=None) -> None:
+    """Slot dest[i]'s page becomes a copy of slot source[i]'s (-1: zeros), all entries as if at once."""
+    dev = pages.block.device
+    ptr, stride, data = _pool(pool, pages)
+    _call(lib.efla_pages_copy, "efla_pages_copy", dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr,
+          stride, data, _slots(source, "source", dev, dest.numel()), _slots(dest, "dest", dev), dest.numel())
+
+
+def efla_pages_free(pages: EflaPages, slots: torch.Tensor, stream=None) -> None:
+    """The slots' pages are free again and the slots empty."""
+    dev = pages.block.device
+    _call(lib.efla_pages_free, "efla_pages_free", dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots,
+          _slots(slots, "slots", dev), slots.numel())
+
+
+def efla_pages_compact(pages: EflaPages, pool, stream=None) -> None:
+    """Moves pages so that the ones in use are the pool's first."""
+    ptr, stride, data = _pool(pool, pages)
+    _call(lib.efla_pages_compact, "efla_pages_compact", pages.block.device, stream, pages.block.data_ptr(),
+          pages.n_pages, pages.n_slots, ptr, stride, data)
+
+
+def _pages_rows(fn, where, pages, pool, rows, slots, stream):
+    dev = pages.block.device
+    ptr, stride, data = _pool(pool, pages)
+    _call(fn, where, dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr, stride,
+          _tensor(rows, "rows", pool.dtype, dev, (slots.numel(), *pool.shape[1:])), data, _slots(slots, "slots", dev),
+          slots.numel())
+
+
+def efla_pages_write(pages: EflaPages, pool, rows: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """rows [n, ...] into the pages of slots[i]."""
+    _pages_rows(lib.efla_pages_write, "efla_pages_write", pages, pool, rows, slots, stream)
+
+
+def efla_pages_read(pages: EflaPages, pool, slots: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """The pages of slots[i] as rows [n, ...] (zero rows for padding when `rows` is not given)."""
+    if rows is None:
+        rows = torch.zeros((slots.numel(), *pool.shape[1:]), dtype=pool.dtype, device=pool.device)
+    _pages_rows(lib.efla_pages_read, "efla_pages_read", pages, pool, rows, slots, stream)
+    return rows
+
+
+def efla_pages_status(pages: EflaPages, clear: bool = False, stream=None) -> int:
+    """EFLA_OK, EFLA_ERR_SLOT or EFLA_ERR_FULL: what the calls on this cache met so far (waits for the stream)."""
+    dev = pages.block.device
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        return int(lib.efla_pages_status(pages.block.data_ptr(), int(clear),
+                                         s.cuda_stream if hasattr(s, "cuda_stream") else int(s)))
+
+
+def efla_scan_step_paged(x, g, pages: EflaPages, pool, slots, source=None, o=None, stream=None,
+                         rule: int = EFLA_RULE_EXACT) -> torch.Tensor:
+    """efla_scan_step on a state cache: row n's state is the page of slot slots[n] in pool [n_pages,H,d] float32.
+    slots [N] int32, -1: a padded row, whose o is left as it was; source [N] int32: the slot a row's entering state is
+    read from instead (-1: a zero state).  Returns o [N,H,d] (zeros for rows left out when `o` is not given)."""
+    N, H, d, gw, dt = _step_shape(x, g)
+    dev = x.device
+    if pool.shape[1:] != x.shape[1:]:
+        raise ValueError(f"pool must be [{pages.n_pages},{H},{d}], got {tuple(pool.shape)}")
+    ptr, stride, _ = _pool(pool, pages, torch.float32)
+    if o is None:
+        o = torch.zeros_like(x)
+    _call(lib.efla_scan_step_paged, "efla_scan_step_paged", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
+          _tensor(g, "g", torch.float32, dev, g.shape), pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr, stride,
+          _slots(slots, "slots", dev, N), _slots(source, "source", dev, N), _tensor(o, "o", x.dtype, dev, x.shape), N, H,
+          d, gw, dt, int(rule))
+    return o
+
+
+def efla_recurrent_step_paged(q, k, v, beta, pages: EflaPages, pool, slots, source=None, g=None, o=None, stream=None,
+                              rule: int = EFLA_RULE_EXACT) -> torch.Tensor:
+    """efla_recurrent_step (with g [N,H] float32: efla_recurrent_step_gated) on a state cache: row n's state is the
+    page of slot slots[n] in pool [n_pages,H,d_k,d_v] float32.  slots, source and o as in efla_scan_step_paged."""
+    dt, dev = k.dtype, k.device
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"k must be [N,H,d_k] and v [N,H,d_v], got {tuple(k.shape)} and {tuple(v.shape)}")
+    N, H, d_k = k.shape
+    d_v = v.shape[-1]
+    if pool.shape[1:] != (H, d_k, d_v):
+        raise ValueError(f"pool must be [{pages.n_pages},{H},{d_k},{d_v}], got {tuple(pool.shape)}")
+    ptr, stride, _ = _pool(pool, pages, torch.float32)
+    if o is None:
+        o = torch.zeros_like(v)
+    _call(lib.efla_recurrent_step_paged, "efla_recurrent_step_paged", dev, stream, _tensor(q, "q", dt, dev, k.shape),
+          _tensor(k, "k", dt, dev, k.shape), _tensor(v, "v", dt, dev, (N, H, d_v)), _tensor(beta, "beta", dt, dev, (N, H)),
+          _tensor(g, "g", torch.float32, dev, (N, H)), pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr, stride,
+          _slots(slots, "slots", dev, N), _slots(source, "source", dev, N), _tensor(o, "o", dt, dev, (N, H, d_v)), N, H,
+          d_k, d_v, _DTYPES.get(dt, -1), int(rule))
+    return o
+
+
+__all__ = ["efla_scan_workspace_bytes", "efla_scan_fwd", "efla_scan_fwd_save", "efla_scan_backward", "efla_scan_step",
+           "efla_scan_step_paged", "efla_recurrent_step_paged", "EflaPages", "new_pages", "efla_pages_fork",
+           "efla_pages_copy", "efla_pages_free", "efla_pages_compact", "efla_pages_write", "efla_pages_read",
+           "efla_pages_status", "EFLA_ERR_SLOT", "EFLA_ERR_FULL",
+           "efla_train_saved_bytes", "efla_chunk_fwd_save", "efla_backward_saved", "efla_chunk_fwd_segmented", "efla_chunk_fwd_varlen", "efla_chunk_fwd_gated", "efla_recurrent_step_gated", "efla_backward", "efla_backward_workspace_bytes", "EFLA_RULE_EXACT", "EFLA_RULE_EULER", "efla_gate", "efla_chunk_fwd", "efla_chunk_fwd_noalloc", "efla_chunk_fwd_workspace_bytes", "efla_recurrent_step",
            "efla_workspace_status", "efla_noalloc_status", "efla_status_string", "load_checked", "efla_selftest_wait_timeout", "new_workspace", "EflaError", "lib",
            "LIB_PATH", "CHUNK"]

@@ -37,6 +37,8 @@ const char* efla_status_string(int status) {
         case EFLA_ERR_CUDA: return "EFLA_ERR_CUDA";
         case EFLA_ERR_TIMEOUT: return "EFLA_ERR_TIMEOUT";
         case EFLA_ERR_BOUNDS: return "EFLA_ERR_BOUNDS";
+        case EFLA_ERR_SLOT: return "EFLA_ERR_SLOT";
+        case EFLA_ERR_FULL: return "EFLA_ERR_FULL";
         default: return "EFLA_ERR_UNKNOWN";
     }
 }

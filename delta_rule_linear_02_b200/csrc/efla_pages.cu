@@ -1,0 +1,309 @@
+// efla_pages.cu -- pages of the state cache: init, free, fork, copy, compact, rows in and out.
+//
+// A page holds the whole recurrent state of one sequence; a slot names a sequence.  Plans (which
+// page goes where) are made by one block from the lists alone, so they are the same on every
+// run; the data then moves with every byte read once and written once.
+#include "efla_kernels.h"
+#include "efla_pages.cuh"
+
+namespace efla {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sum of a 0/1 flag over the block, in thread order; *total: the block's sum.
+__device__ __forceinline__ int block_rank(bool flag, int* total) {
+    __shared__ int warps[33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned mask = __ballot_sync(0xffffffffu, flag);
+    __syncthreads();
+    if (lane == 0) warps[warp] = __popc(mask);
+    __syncthreads();
+    if (warp == 0) {
+        const int own = warps[lane];
+        int sum = own;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += up;
+        }
+        warps[lane] = sum - own;
+        if (lane == 31) warps[32] = sum;
+    }
+    __syncthreads();
+    *total = warps[32];
+    return warps[warp] + __popc(mask & ((1u << lane) - 1u));
+}
+
+__global__ void pages_init_kernel(PagesBlock b) {
+    const int words = b.n_slots + b.n_pages;
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < kPagesHeader) reinterpret_cast<int*>(b.err)[i] = 0;
+    if (i < words) b.table[i] = -1;                              // table and owners are adjacent
+    if (i < b.n_slots + 2 * b.n_pages) b.claim[i] = 0;           // claims and the move list too
+}
+
+__global__ void pages_free_kernel(PagesBlock b, const int* __restrict__ slots, int n) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    const int s = slots[i];
+    if (s == -1) return;
+    // a slot listed twice gives its page back once; the second time it is empty, an error
+    const int page = s < 0 || s >= b.n_slots ? -1 : atomicExch(&b.table[s], -1);
+    if (page < 0 || page >= b.n_pages) atomicOr(b.err, kPagesBadSlot);
+    else b.owner[page] = -1;
+}
+
+// The lowest of the entries that name a slot claims it (entry i claims with n - i, so the
+// largest claim wins and an unclaimed slot is zero).
+__device__ __forceinline__ void claim_slots(const PagesBlock& b, const int* dest, int n) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int s = dest[i];
+        if (s >= 0 && s < b.n_slots) atomicMax(&b.claim[s], n - i);
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void release_claims(const PagesBlock& b, const int* dest, int n) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int s = dest[i];
+        if (s >= 0 && s < b.n_slots) b.claim[s] = 0;
+    }
+}
+
+// Entry i of a fork (fresh: the destination has no page yet) or a copy (it has one) in order.
+// *page: the source's page, -1 for a zeroed one.
+__device__ __forceinline__ bool plan_entry(const PagesBlock& b, const int* source, const int* dest, int n, int i,
+                                           bool fresh, int* page) {
+    if (i >= n) return false;
+    const int s = dest[i];
+    if (s == -1) return false;
+    bool ok = s >= 0 && s < b.n_slots && b.claim[s] == n - i;
+    if (ok) {
+        const int has = b.table[s];
+        ok = fresh ? has == -1 : has >= 0 && has < b.n_pages;
+    }
+    const int from = source[i];
+    *page = -1;
+    if (ok && from != -1) {
+        ok = from >= 0 && from < b.n_slots;
+        if (ok) *page = b.table[from];
+        ok = ok && *page >= 0 && *page < b.n_pages;
+    }
+    if (!ok) atomicOr(b.err, kPagesBadSlot);
+    return ok;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pages_fork_plan(PagesBlock b, const int* source, const int* dest,
+                                                                int n) {
+    claim_slots(b, dest, n);
+    int count = 0;
+    for (int base = 0; base < n; base += kPlanThreads) {
+        const int i = base + threadIdx.x;
+        int page, total;
+        const bool ok = plan_entry(b, source, dest, n, i, true, &page);
+        const int r = count + block_rank(ok, &total);
+        if (ok && r < b.n_pages) {
+            b.src[r] = page;
+            b.dst[r] = dest[i];          // the slot, until it has a page
+        }
+        count += total;
+    }
+    const int wanted = count;
+    count = min(count, b.n_pages);
+    release_claims(b, dest, n);
+    // the r-th entry gets the r-th free page
+    int free_pages = 0;
+    for (int base = 0; base < b.n_pages && free_pages < count; base += kPlanThreads) {
+        const int p = base + threadIdx.x;
+        int total;
+        const bool is_free = p < b.n_pages && b.owner[p] == -1;
+        const int r = free_pages + block_rank(is_free, &total);
+        if (is_free && r < count) {
+            const int s = b.dst[r];
+            b.owner[p] = s;
+            b.table[s] = p;
+            b.dst[r] = p;
+        }
+        free_pages += total;
+    }
+    if (threadIdx.x == 0) {
+        if (free_pages < wanted) atomicOr(b.err, kPagesFull);
+        *b.moves = min(free_pages, count);
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pages_copy_plan(PagesBlock b, const int* source, const int* dest,
+                                                                int n) {
+    claim_slots(b, dest, n);
+    int count = 0;
+    for (int base = 0; base < n; base += kPlanThreads) {
+        const int i = base + threadIdx.x;
+        int page, total;
+        bool ok = plan_entry(b, source, dest, n, i, false, &page);
+        ok = ok && source[i] != dest[i];
+        const int r = count + block_rank(ok, &total);
+        if (ok && r < b.n_pages) {
+            b.src[r] = page;
+            b.dst[r] = b.table[dest[i]];
+        }
+        count += total;
+    }
+    release_claims(b, dest, n);
+    if (threadIdx.x == 0) *b.moves = min(count, b.n_pages);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pages_compact_plan(PagesBlock b) {
+    int live = 0;
+    for (int base = 0; base < b.n_pages; base += kPlanThreads) {
+        const int p = base + threadIdx.x;
+        int total;
+        block_rank(p < b.n_pages && b.owner[p] >= 0, &total);
+        live += total;
+    }
+    // the r-th page in use from `live` on goes into the r-th free page before it
+    int holes = 0, late = 0;
+    for (int base = 0; base < b.n_pages; base += kPlanThreads) {
+        const int p = base + threadIdx.x;
+        const bool used = p < b.n_pages && b.owner[p] >= 0;
+        int total;
+        const bool hole = p < live && !used, move = p >= live && used;
+        int r = holes + block_rank(hole, &total);
+        if (hole) b.dst[r] = p;
+        holes += total;
+        r = late + block_rank(move, &total);
+        if (move) b.src[r] = p;
+        late += total;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < late; r += kPlanThreads) {
+        const int from = b.src[r], to = b.dst[r], s = b.owner[from];
+        b.owner[to] = s;
+        b.owner[from] = -1;
+        if (s < b.n_slots) b.table[s] = to;
+        else atomicOr(b.err, kPagesBadSlot);
+    }
+    if (threadIdx.x == 0) *b.moves = late;
+}
+
+// The planned moves, where no page is both read and written.
+__global__ void __launch_bounds__(256) pages_move_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs) {
+    const long total = (long)*b.moves * vecs;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+        const int m = (int)(i / vecs);
+        const size_t at = (size_t)(i % vecs) * 16;
+        const int from = b.src[m];
+        const uint4 v = from < 0 ? make_uint4(0, 0, 0, 0)
+                                 : *reinterpret_cast<const uint4*>(pool + (size_t)from * page_bytes + at);
+        *reinterpret_cast<uint4*>(pool + (size_t)b.dst[m] * page_bytes + at) = v;
+    }
+}
+
+// The planned moves as if all at once: a block owns a strip of `width` 16-byte columns of every
+// page, reads it for all moves into shared memory, then writes it.
+__global__ void __launch_bounds__(256) pages_strip_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs,
+                                                          int width) {
+    extern __shared__ uint4 held[];
+    const long c0 = (long)blockIdx.x * width;
+    const int w = (int)min((long)width, vecs - c0), total = *b.moves * w;
+    for (int i = threadIdx.x; i < total; i += 256) {
+        const int m = i / w;
+        const int from = b.src[m];
+        held[i] = from < 0 ? make_uint4(0, 0, 0, 0)
+                           : *reinterpret_cast<const uint4*>(pool + (size_t)from * page_bytes + (c0 + i % w) * 16);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += 256) {
+        const int m = i / w;
+        *reinterpret_cast<uint4*>(pool + (size_t)b.dst[m] * page_bytes + (c0 + i % w) * 16) = held[i];
+    }
+}
+
+// Rows into the pages of their slots (write) or out of them; one block per 4 KiB of a row.
+__global__ void __launch_bounds__(256) pages_rows_kernel(PagesBlock b, char* pool, size_t page_bytes, char* rows,
+                                                         size_t row_bytes, const int* __restrict__ slots, int n,
+                                                         int pieces, bool write) {
+    const int i = blockIdx.x / pieces;
+    const size_t at = ((size_t)(blockIdx.x % pieces) * 256 + threadIdx.x) * 16;
+    const int s = slots[i];
+    if (s == -1) return;
+    bool bad = s < 0 || s >= b.n_slots;
+    const int page = bad ? -1 : b.table[s];
+    bad |= page < 0 || page >= b.n_pages;
+    if (write)                                   // of rows for one slot the first is taken
+        for (int m = threadIdx.x; m < i; m += 256) bad |= slots[m] == s;
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) atomicOr(b.err, kPagesBadSlot);
+        return;
+    }
+    if (at >= row_bytes) return;
+    uint4* cached = reinterpret_cast<uint4*>(pool + (size_t)page * page_bytes + at);
+    uint4* row = reinterpret_cast<uint4*>(rows + (size_t)i * row_bytes + at);
+    if (write) *cached = *row;
+    else *row = *cached;
+}
+
+int move_grid() {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms * 8;
+}
+
+}  // namespace
+
+cudaError_t launch_pages_init(const PagesBlock& b, cudaStream_t stream) {
+    const int words = b.n_slots + 2 * b.n_pages + kPagesHeader;
+    pages_init_kernel<<<(words + 255) / 256, 256, 0, stream>>>(b);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_free(const PagesBlock& b, const int* slots, int n, cudaStream_t stream) {
+    pages_free_kernel<<<(n + 255) / 256, 256, 0, stream>>>(b, slots, n);
+    return cudaGetLastError();
+}
+
+static cudaError_t launch_moves(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes,
+                                cudaStream_t stream) {
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    pages_move_kernel<<<move_grid(), 256, 0, stream>>>(b, static_cast<char*>(pool), page_bytes, (long)(data_bytes / 16));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes, const int* source,
+                              const int* dest, int n, cudaStream_t stream) {
+    pages_fork_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
+    if (!pool) return cudaGetLastError();
+    return launch_moves(b, pool, page_bytes, data_bytes, stream);
+}
+
+cudaError_t launch_pages_compact(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes,
+                                 cudaStream_t stream) {
+    pages_compact_plan<<<1, kPlanThreads, 0, stream>>>(b);
+    return launch_moves(b, pool, page_bytes, data_bytes, stream);
+}
+
+cudaError_t launch_pages_copy(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes, const int* source,
+                              const int* dest, int n, cudaStream_t stream) {
+    pages_copy_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    constexpr int kHeld = kPagesCopyMax * 16;
+    static std::atomic<uint64_t> done{0};
+    if ((e = set_smem_limit_once(pages_strip_kernel, kHeld, done)) != cudaSuccess) return e;
+    const long vecs = (long)(data_bytes / 16);
+    const int width = (int)(vecs < kPagesCopyMax / n ? vecs : kPagesCopyMax / n);
+    pages_strip_kernel<<<(unsigned)((vecs + width - 1) / width), 256, (size_t)n * width * 16, stream>>>(
+        b, static_cast<char*>(pool), page_bytes, vecs, width);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_rows(const PagesBlock& b, void* pool, size_t page_bytes, void* rows, size_t row_bytes,
+                              const int* slots, int n, bool write, cudaStream_t stream) {
+    const int pieces = (int)((row_bytes + 4095) / 4096);
+    pages_rows_kernel<<<(unsigned)((long)n * pieces), 256, 0, stream>>>(b, static_cast<char*>(pool), page_bytes,
+                                                                       static_cast<char*>(rows), row_bytes, slots, n,
+                                                                       pieces, write);
+    return cudaGetLastError();
+}
+
+}  // namespace efla

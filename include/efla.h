@@ -46,7 +46,9 @@ typedef enum {
     EFLA_ERR_UNSUPPORTED = 2,  /* valid but unsupported shape (d_k, d_v, chunk) or dtype */
     EFLA_ERR_CUDA = 3,         /* a CUDA call or kernel launch failed */
     EFLA_ERR_TIMEOUT = 4,      /* a device-side bounded wait ran out (see efla_workspace_status) */
-    EFLA_ERR_BOUNDS = 5        /* a checked build (libefla_checked.so) recorded an out-of-range access */
+    EFLA_ERR_BOUNDS = 5,       /* a checked build (libefla_checked.so) recorded an out-of-range access */
+    EFLA_ERR_SLOT = 6,         /* a list given to a state cache named a wrong slot (see efla_pages_status) */
+    EFLA_ERR_FULL = 7          /* a state cache had no free page left (see efla_pages_status) */
 } efla_status;
 
 typedef enum {
@@ -399,6 +401,133 @@ int efla_backward_saved(const void *q, const void *k, const void *v, const void 
                         const float *dS_T, float *dq, float *dk, float *dv, float *dbeta, float *dS0, int B,
                         int H, int T, int d_k, int d_v, int dtype, int rule, const void *saved,
                         size_t saved_bytes, void *workspace, size_t workspace_bytes, efla_stream_t stream);
+
+/*
+ * The per-channel gated recurrence: a vector state per stream instead of a matrix, each channel
+ * with its own decay and no key (the recurrent layers that hybrid models put beside the delta
+ * rule).  The gated flow's conventions carry over: g is a log-decay (a forget gate e^{g};
+ * g <= 0 decays), and one token is the exact flow of dh/dtau = g h + x over its unit interval,
+ *     h_t = e^{g_t} h_{t-1} + phi(g_t) x_t,   o_t = h_t,   phi(g) = (e^g - 1) / g, phi(0) = 1;
+ * EFLA_RULE_EULER writes with 1 in the place of phi.  g = -inf forgets everything and, under the
+ * exact rule, writes nothing (phi = 0).
+ *
+ *   x, o  [B,H,T,d] (dtype);  g float32, [B,H,T,d] (g_width = d) or [B,H,T] (g_width = 1: one
+ *   decay for all channels of a head);  S0, S_T [B,H,d] float32.
+ * Packed batches: with cu_seqlens (a HOST array of B + 1 offsets as in efla_chunk_fwd_varlen, T =
+ * cu_seqlens[B]) the tensors are [H,T,d], [H,T,(d)] and every sequence runs from its own S0 row;
+ * an empty one passes its state through.  The offsets are copied to the workspace (from pageable
+ * memory that copy may synchronise the host with `stream`, and it cannot be captured).
+ * Supported: d up to 4096 with d * sizeof(dtype) a multiple of 16 bytes; any T >= 0 and B, H >= 0.
+ *
+ * efla_scan_workspace_bytes -- workspace of efla_scan_fwd (packed != 0: with cu_seqlens), 0 for
+ * arguments it would reject.  Its first bytes hold a sticky device error word (a wait that ran out;
+ * efla_workspace_status; zero it once before first use if it is to be read).
+ *
+ * efla_scan_fwd -- the forward.  S0 NULL: zero states.  S_T may be NULL (not wanted) or alias S0;
+ * otherwise no output may overlap an input, the workspace or another output.  All pointers
+ * 16-byte aligned.  The results are the same bits on every call.  After the call the workspace
+ * also holds the states that efla_scan_backward starts its chunks from: kept unmodified, it is
+ * that call's `saved`.
+ */
+size_t efla_scan_workspace_bytes(int B, int H, int T, int d, int g_width, int dtype, int packed);
+int efla_scan_fwd(const void *x, const float *g, const int *cu_seqlens, const float *S0, void *o, float *S_T, int B,
+                  int H, int T, int d, int g_width, int dtype, int rule, void *workspace, size_t workspace_bytes,
+                  efla_stream_t stream);
+
+/*
+ * efla_scan_backward -- gradients of efla_scan_fwd for the loss sum(dO * o) + sum(dS_T * S_T).  With
+ * G_t = dL/dh_t = dO_t + e^{g_{t+1}} G_{t+1} (the last token: dO + dS_T):
+ *   dx_t = phi(g_t) G_t,  dg_t = G_t (e^{g_t} h_{t-1} + phi'(g_t) x_t)  (summed over the channels
+ *   for g_width = 1),  dS0 = e^{g_0} G_0.
+ *   x, g, S0 as in the forward, dO [B,H,T,d] (dtype), dS_T [B,H,d] float32 or NULL (zero)
+ *   dx [B,H,T,d], dg (g's shape), dS0 [B,H,d]: float32 outputs, dS0 may be NULL (not wanted)
+ *   saved: the workspace of the efla_scan_fwd call with the same x, g, cu_seqlens, S0 and rule, or
+ *   NULL: the states are computed again.  No output or the workspace may overlap an input, `saved`
+ *   or each other.  The results are the same bits on every call.
+ */
+size_t efla_scan_backward_workspace_bytes(int B, int H, int T, int d, int g_width, int dtype, int packed, int saved);
+int efla_scan_backward(const void *x, const float *g, const int *cu_seqlens, const float *S0, const void *dO,
+                       const float *dS_T, float *dx, float *dg, float *dS0, int B, int H, int T, int d, int g_width,
+                       int dtype, int rule, const void *saved, size_t saved_bytes, void *workspace,
+                       size_t workspace_bytes, efla_stream_t stream);
+
+/*
+ * efla_scan_step -- one token of the recurrence above for N rows, states updated in place:
+ *   x, o [N,H,d] (dtype), g float32 [N,H,d] or [N,H], S [N,H,d] float32.
+ */
+int efla_scan_step(const void *x, const float *g, float *S, void *o, int N, int H, int d, int g_width, int dtype,
+                   int rule, efla_stream_t stream);
+
+/*
+ * The state cache of a server.  A recurrent sequence's cache is its state, of one size for every
+ * length: a page holds one sequence's state (of one layer, or of all), a slot names a sequence,
+ * and every page belongs to one slot at most (each token rewrites the whole state, so pages are
+ * not shared).  The caller owns two buffers:
+ *   pool   n_pages pages, page p at pool + p * page_bytes (16-byte aligned; page_bytes a multiple
+ *          of 16).  A call works on data_bytes of each page from `pool` on, so that a page may
+ *          hold several layers and a step is given the pool at its layer's offset.
+ *   pages  the block, efla_pages_bytes(n_pages, n_slots) bytes, 16-byte aligned, in int32 words:
+ *          64 of header (word 0: errors), n_slots of table (slot -> page, -1: none), n_pages of
+ *          owners (page -> slot, -1: free), then scratch (zero between calls as efla_pages_init
+ *          leaves it).
+ * Lists of slots are int32 device arrays; an entry -1 is padding and skipped.  The calls plan on
+ * the device: they never synchronise, can be captured and replayed, and give the same result on
+ * every run.  Calls on one block have to be ordered by streams or events.
+ * A wrong entry (a slot out of range; one without a page where a page is needed, or with one
+ * where none may be; a destination listed twice: the first entry is taken) is left out, touches
+ * nothing, and sets an error that efla_pages_status reports: EFLA_ERR_SLOT, or EFLA_ERR_FULL for
+ * entries that found no free page.
+ *
+ * efla_pages_init -- every slot empty, every page free.
+ * efla_pages_fork -- entry i gives the empty slot dest[i] the lowest free page (in order of i)
+ *   with a copy of the page of slot source[i], or zeros for source[i] = -1.  Sources are looked up
+ *   as they were before the call.  pool NULL: pages are given without copying (their content is
+ *   whatever it was), for a step that reads from `source` itself.
+ * efla_pages_copy -- the page of slot dest[i] becomes a copy of that of source[i] (-1: zeros), all
+ *   entries as if at once: sources are read as they were before the call, so slots may exchange
+ *   their states.  At most 8192 entries (else EFLA_ERR_UNSUPPORTED).
+ * efla_pages_free -- the slots' pages are free and the slots empty.
+ * efla_pages_compact -- moves pages so that the ones in use are the first of the pool: the k-th
+ *   page in use behind the count of pages in use goes into the k-th free page before it.
+ * efla_pages_write / efla_pages_read -- rows [n, row_bytes] into the pages of slots[i] / out of
+ *   them (a prefill's final states into the cache, a sequence's state out to elsewhere); rows of
+ *   entries that are left out are not touched.  row_bytes is the call's data_bytes.
+ * efla_pages_status -- waits for `stream` and reports the errors of the calls so far (clear != 0:
+ *   forgets them).  The only call that synchronises the host.
+ */
+size_t efla_pages_bytes(int n_pages, int n_slots);
+int efla_pages_init(void *pages, size_t pages_bytes, int n_pages, int n_slots, efla_stream_t stream);
+int efla_pages_fork(void *pages, int n_pages, int n_slots, void *pool, size_t page_bytes, size_t data_bytes,
+                    const int *source, const int *dest, int n, efla_stream_t stream);
+int efla_pages_copy(void *pages, int n_pages, int n_slots, void *pool, size_t page_bytes, size_t data_bytes,
+                    const int *source, const int *dest, int n, efla_stream_t stream);
+int efla_pages_free(void *pages, int n_pages, int n_slots, const int *slots, int n, efla_stream_t stream);
+int efla_pages_compact(void *pages, int n_pages, int n_slots, void *pool, size_t page_bytes, size_t data_bytes,
+                       efla_stream_t stream);
+int efla_pages_write(void *pages, int n_pages, int n_slots, void *pool, size_t page_bytes, const void *rows,
+                     size_t row_bytes, const int *slots, int n, efla_stream_t stream);
+int efla_pages_read(void *pages, int n_pages, int n_slots, const void *pool, size_t page_bytes, void *rows,
+                    size_t row_bytes, const int *slots, int n, efla_stream_t stream);
+int efla_pages_status(void *pages, int clear, efla_stream_t stream);
+
+/*
+ * efla_recurrent_step_paged -- efla_recurrent_step_ex (g NULL) or efla_recurrent_step_gated on a state
+ * cache: row n's state is [H,d_k,d_v] float32 at the start of the page of slot slots[n].
+ * efla_scan_step_paged -- efla_scan_step on a state cache, row n's state [H,d] float32.
+ *   source (may be NULL): row n reads its entering state from the page of slot source[n] instead
+ *   (-1: a zero state) and writes its own: a fork, or a fresh sequence, without a copy of its own.
+ *   slots[n] = -1 is a padded row: its o is left as it was.  A row is left out with EFLA_ERR_SLOT
+ *   (efla_pages_status) if its slot or source is wrong or has no page, if an earlier row has its
+ *   slot, or if its source (another slot than its own) is the slot of a row of this call.
+ *   No other argument may overlap pool, pages or o.
+ */
+int efla_recurrent_step_paged(const void *q, const void *k, const void *v, const void *beta, const float *g,
+                              void *pages, int n_pages, int n_slots, float *pool, size_t page_bytes, const int *slots,
+                              const int *source, void *o, int N, int H, int d_k, int d_v, int dtype, int rule,
+                              efla_stream_t stream);
+int efla_scan_step_paged(const void *x, const float *g, void *pages, int n_pages, int n_slots, float *pool,
+                         size_t page_bytes, const int *slots, const int *source, void *o, int N, int H, int d,
+                         int g_width, int dtype, int rule, efla_stream_t stream);
 
 #ifdef __cplusplus
 }
