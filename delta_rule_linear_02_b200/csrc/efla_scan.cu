@@ -1,4 +1,24 @@
 // efla_scan.cu -- the per-channel gated linear recurrence: forward, backward, one token.
+//
+// The recurrence is affine in the state: over any run of tokens h_out = A h_in + B, and runs
+// compose.  A tile is 64 tokens x 128 channels (a "strip"); its eight compute warps take eight
+// tokens each, a lane four channels.  Per tile:
+//   1. every compute thread reduces its run to (A, B), which goes to shared memory;
+//   2. the chain warps (a thread per channel) publish the tile's (A, B), put the state entering
+//      the tile together from the preceding tiles of the strip (look back: the state that entered
+//      a tile some steps before and the (A, B) since, in token order), publish the state leaving
+//      the tile, and hand every run the state entering it;
+//   3. every compute thread continues its run from there and writes the outputs.
+// Inputs are staged by bulk copies some tiles ahead, and are read from memory once.
+//
+// What is published is its own signal: a word that is not there yet holds a bit pattern that no
+// result has (all ones), so publishing takes one store and reading it one load, without fences
+// or flags.  The state leaving a tile is always fma(A, entering, B) of the same numbers, wherever
+// the look back started, so results do not depend on timing.  The grid is launched cooperatively:
+// all blocks are resident and take tiles in time order (block b: tiles b, b + grid, ...), so
+// every wait is for a tile that a running block has begun or finished; each wait is bounded.
+#include <cooperative_groups.h>
+
 #include "efla_kernels.h"
 #include "efla_pages.cuh"
 #include "efla_scan.cuh"
@@ -8,36 +28,29 @@ namespace efla {
 using namespace sm100;
 namespace {
 
-struct V4 {
-    float v[4];
+struct P4 {          // four channels
+    float2 lo, hi;
 };
+__device__ __forceinline__ P4 all4(float x) { return P4{both(x), both(x)}; }
+__device__ __forceinline__ P4 fma4(const P4& a, const P4& b, const P4& c) {
+    return P4{fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
+}
+__device__ __forceinline__ P4 mul4(const P4& a, const P4& b) { return P4{mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ P4 add4(const P4& a, const P4& b) { return P4{add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
 template <typename T>
-__device__ __forceinline__ V4 ld4(const T* p) {
+__device__ __forceinline__ P4 ld4(const T* p) {
     const float4 f = load4(p);
-    return V4{{f.x, f.y, f.z, f.w}};
+    return P4{make_float2(f.x, f.y), make_float2(f.z, f.w)};
 }
 template <typename T>
-__device__ __forceinline__ void st4(T* p, const V4& v) {
-    store4(p, make_float4(v.v[0], v.v[1], v.v[2], v.v[3]));
+__device__ __forceinline__ void st4(T* p, const P4& v) {
+    store4(p, make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y));
 }
-__device__ __forceinline__ V4 zero4() { return V4{{0.f, 0.f, 0.f, 0.f}}; }
 
-// ---------------------------------------------------------------- tiles
-// The recurrence is affine in the state: over any run of tokens h_out = A h_in + B, and runs
-// compose.  A tile is 32 tokens x 128 channels (a "strip"): its eight warps take four tokens
-// each, a lane four channels, so a thread's run lives in registers and is read from memory once.
-//   1. every thread reduces its run to (A, B); the warps exchange them in shared memory;
-//   2. the tile's (A, B) is published, the state entering the tile is put together from the
-//      preceding tiles of the strip (look back: the nearest published state, then the published
-//      (A, B) after it, in token order), and the state leaving the tile is published;
-//   3. every thread continues its run from the state entering it and writes the outputs.
-// A tile's leaving state is always fma(A, entering, B) of the same numbers, wherever the look
-// back started, so results do not depend on timing.  The grid is launched cooperatively: all
-// blocks are resident and take tiles in time order (block b: tiles b, b + grid, ...), so every
-// wait is for a tile that a running block has already begun or finished, and each is bounded.
 constexpr int kTok = kScanChunk, kWarps = 8, kRun = kTok / kWarps, kCh = 128;
-constexpr int kThreads = kWarps * 32;
+constexpr int kComputeThreads = kWarps * 32, kThreads = kComputeThreads + kCh;
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kBack = 16;          // most (A, B) that one look back folds
 
 // How lanes map to (stream, channel): heads of d channels with 32 % (d / 4) == 0 are packed
 // side by side into a strip; other widths up to 128 take a strip each, wider ones several.
@@ -75,8 +88,9 @@ __device__ __forceinline__ Lane lane_of(const Strips& S, long Z, int d, int stri
         L.z = strip / S.per_head;
         L.c = (part * 32 + lane) * 4;
         L.on = L.c < d;
-        L.smem = S.per_head > 1 ? lane * 4 : L.c;
+        L.smem = lane * 4;
         L.row = S.per_head > 1 ? kCh : d;
+        if (!L.on) L.smem = 0;       // read something that is there, use nothing of it
     }
     return L;
 }
@@ -92,10 +106,11 @@ __device__ __forceinline__ void stage(T* dst, const T* src, const Strips& S, lon
         const long z = (long)strip * S.heads + lane;
         if (lane < S.heads && z < Z)
             bulk_load(dst + lane * kTok * d, src + (z * Ttot + t0) * d, rows * d * (int)sizeof(T), bar);
-    } else if (lane < rows) {
+    } else {
         const long z = strip / S.per_head;
         const int c0 = (strip % S.per_head) * kCh;
-        bulk_load(dst + lane * kCh, src + (z * Ttot + t0 + lane) * d + c0, min(kCh, d - c0) * (int)sizeof(T), bar);
+        for (int t = lane; t < rows; t += 32)
+            bulk_load(dst + t * kCh, src + (z * Ttot + t0 + t) * d + c0, min(kCh, d - c0) * (int)sizeof(T), bar);
     }
 }
 __device__ __forceinline__ int strip_channels(const Strips& S, long Z, int d, int strip) {
@@ -103,162 +118,222 @@ __device__ __forceinline__ int strip_channels(const Strips& S, long Z, int d, in
     return S.per_head == 1 ? d : min(kCh, d - (strip % S.per_head) * kCh);
 }
 
-// Which of the tile's tokens begin or end a sequence (bit l: token t0 + l), and, per lane, the
-// sequence that token t0 + lane belongs to.
-struct Marks {
-    uint32_t first, last;
-    int n;
-};
-__device__ __forceinline__ Marks tile_marks(const int* cu, int nseq, int T, int t0) {
-    Marks m{t0 == 0 ? 1u : 0u, 0u, 0};
-    const int t = t0 + (threadIdx.x & 31);
-    if (!cu) {
-        if (T - t0 <= kTok) m.last = 1u << (T - 1 - t0);
-        return m;
-    }
-    int lo = 0, hi = nseq;               // the largest n with cu[n] <= t: the sequence that holds t
+// The packed sequence that holds token t: the largest n with cu[n] <= t.
+__device__ __forceinline__ int seq_of(const ScanArgs& P, int t) {
+    if (!P.cu) return 0;
+    int lo = 0, hi = P.nseq;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid;
+        if (P.cu[mid] <= t) lo = mid;
         else hi = mid;
     }
-    m.n = lo;
-    m.first = __ballot_sync(0xffffffffu, t < T && cu[lo] == t);
-    m.last = __ballot_sync(0xffffffffu, t < T && cu[lo + 1] == t + 1);
-    return m;
+    return lo;
 }
 
-__device__ __forceinline__ int load_acquire(const int* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void store_release(int* p, int v) {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// What the tiles of a strip publish, by step (chunk in the direction of the recurrence) and strip:
-// flag 1: the tile's (A, B); 2: also the state leaving it, stored as the state entering the next.
-enum : int { kAgg = 1, kState = 2 };
+// What the tiles of a strip publish, by step (chunk in the direction of the recurrence) and strip,
+// and which of a chunk's tokens begin or end a sequence (bit l: token l; packed batches).
 struct Chain {
-    int* flag;          // [steps][strips]
-    float2* agg;        // [steps][strips][128]
-    float* state;       // [steps][strips][128]: entering
+    unsigned long long* agg;     // [steps][strips][128]: A, B
+    float* state;                // [steps][strips][128]: entering
+    ulonglong2* marks;           // [chunks]: first, last
     int strips, steps;
 };
+constexpr unsigned long long kNoAgg = ~0ull;
+constexpr uint32_t kNoState = ~0u;
+// A of a run with a sequence's begin in it: what came before does not matter, not even a NaN.
+// (No product of decays is -0.)
+constexpr float kCut = -0.0f;
+__device__ __forceinline__ float run_on(float A, float h, float B) {
+    return __float_as_uint(A) == 0x80000000u ? B : fmaf(A, h, B);
+}
 
-// Threads 0 .. 127 of the block, thread k for channel k of the strip: publishes the tile's (A, B),
-// returns the state entering the tile and publishes the one leaving it.  `reset`: A is zero, the
-// leaving state does not depend on the entering one; `fresh`: the entering state is not needed.
-__device__ __forceinline__ float chain_step(const Chain& C, int step, int strip, float A, float B, bool reset,
-                                            bool fresh, bool* dead, int* window, uint32_t* err) {
-    const int k = threadIdx.x;
-    const size_t at = (size_t)step * C.strips + strip;
+__device__ __forceinline__ unsigned long long load_word(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t load_word(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void publish(unsigned long long* p, float A, float B) {
+    // a NaN that happens to have the pattern is made the usual one
+    uint32_t b = __float_as_uint(B);
+    if (b == ~0u) b = 0x7fffffffu;
+    const unsigned long long v = (unsigned long long)b << 32 | __float_as_uint(A);
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ void publish(float* p, float h) {
+    uint32_t b = __float_as_uint(h);
+    if (b == ~0u) b = 0x7fffffffu;
+    asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(b) : "memory");
+}
+
+// Before the first tile: nothing is published, the chunks' marks, states of empty sequences.
+// All blocks pass the grid's barrier before any of them looks at another's words.
+__device__ __forceinline__ void begin_chain(const ScanArgs& P, const Chain& C, const float* in, float* out) {
+    const long words = (long)C.steps * C.strips * kCh, all = (long)gridDim.x * kThreads;
+    const long me = (long)blockIdx.x * kThreads + threadIdx.x;
+    if (C.steps > 1)
+        for (long i = me; i < words; i += all) {
+            C.agg[i] = kNoAgg;
+            reinterpret_cast<uint32_t*>(C.state)[i] = kNoState;
+        }
+    if (P.cu) {
+        const int lane = threadIdx.x & 31;
+        for (long s = me / 32; s < C.steps; s += all / 32) {
+            unsigned long long first = 0, last = 0;
+            for (int half = 0; half < 2; ++half) {
+                const int t = (int)s * kTok + half * 32 + lane;
+                const int n = t < P.T ? seq_of(P, t) : 0;
+                first |= (unsigned long long)__ballot_sync(0xffffffffu, t < P.T && P.cu[n] == t) << (half * 32);
+                last |= (unsigned long long)__ballot_sync(0xffffffffu, t < P.T && P.cu[n + 1] == t + 1) << (half * 32);
+            }
+            if (lane == 0) C.marks[s] = make_ulonglong2(first, last);
+        }
+        if (out)
+            for (int n = blockIdx.x; n < P.nseq; n += gridDim.x)
+                if (P.cu[n] == P.cu[n + 1])
+                    for (long i = threadIdx.x; i < P.Z * P.d; i += kThreads)
+                        out[n * P.Z * P.d + i] = in ? in[n * P.Z * P.d + i] : 0.f;
+    }
+    if (C.steps > 1 || P.cu) cooperative_groups::this_grid().sync();
+}
+__device__ __forceinline__ ulonglong2 chunk_marks(const ScanArgs& P, const Chain& C, int chunk) {
+    if (P.cu) return __ldcg(C.marks + chunk);
+    const int left = P.T - chunk * kTok;
+    return make_ulonglong2(chunk == 0 ? 1ull : 0ull, left <= kTok ? 1ull << (left - 1) : 0ull);
+}
+
+// Thread k of the chain warps, channel k of the strip: publishes the tile's (A, B), returns the
+// state entering the tile and publishes the one leaving it.  `reset`: A is zero, the leaving state
+// does not depend on the entering one; `fresh`: the entering state is not needed.
+__device__ __forceinline__ float chain_step(const Chain& C, int step, int strip, int k, float A, float B, bool reset,
+                                            bool fresh, bool* dead, uint32_t* err) {
+    const size_t at = ((size_t)step * C.strips + strip) * kCh + k, up = (size_t)C.strips * kCh;
     const bool more = step + 1 < C.steps;
-    if (reset) {
-        if (more) {
-            C.state[(at + C.strips) * kCh + k] = B;
-            __threadfence();
-            bar_sync(1, kCh);
-            if (k == 0) store_release(C.flag + at, kState);
-        }
-        if (fresh) return 0.f;
-    } else if (more) {
-        C.agg[at * kCh + k] = make_float2(A, B);
-        __threadfence();
-        bar_sync(1, kCh);
-        if (k == 0) store_release(C.flag + at, kAgg);
+    if (more) {
+        if (reset) publish(C.state + at + up, B);
+        publish(C.agg + at, reset ? kCut : A, B);
     }
-    if (k < 32) {       // the nearest preceding tile with a state, all tiles after it with (A, B)
-        const int p = step - 1 - k;
-        const int* flag = C.flag + (size_t)p * C.strips + strip;
-        int found = -1;
-        uint64_t begin = 0;
-        for (;;) {
-            const int f = p >= 0 ? load_acquire(flag) : 0;
-            const uint32_t state = __ballot_sync(0xffffffffu, f == kState);
-            const uint32_t any = __ballot_sync(0xffffffffu, f != 0);
-            const int j = __ffs(state) - 1;
-            if (j >= 0 && (any & ((1u << j) - 1u)) == (1u << j) - 1u) {
-                found = j;
-                break;
-            }
-            if (*dead) break;
-            const uint64_t now = globaltimer_ns();
-            if (begin == 0) begin = now;
-            if (__any_sync(0xffffffffu, now - begin > kWaitNs)) {
-                if (k == 0) atomicOr(err, kDevTimeout);
-                *dead = true;
-                break;
-            }
-        }
-        if (k == 0) *window = found;
-    }
-    bar_sync(1, kCh);
-    const int j = *window;
-    float h = 0.f;
-    if (j >= 0) {
-        h = __ldcg(C.state + (at - (size_t)j * C.strips) * kCh + k);
-        const float2* agg = C.agg + (at - (size_t)j * C.strips) * kCh + k;
-        for (int i = 0; i < j; i += 8) {
-            float2 ab[8];
+    if (fresh) return 0.f;
+    // the tiles of this grid's wave before this one publish (A, B) without waiting for states; the
+    // state before them comes from an earlier wave
+    const int J = min(min((int)blockIdx.x / C.strips, kBack), step - 1);
+    const unsigned long long* agg = C.agg + at - J * up;
+    const uint32_t* root = reinterpret_cast<const uint32_t*>(C.state) + (at - J * up);
+    unsigned long long ab[kBack];
+    uint32_t h0 = load_word(root);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (i + u < j) ab[u] = __ldcg(agg + (size_t)(i + u) * C.strips * kCh);
+    for (int i = 0; i < kBack; ++i) ab[i] = i < J ? load_word(agg + i * up) : 0ull;
+    uint64_t begin = 0;
+    for (;;) {
+        bool missing = h0 == kNoState;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (i + u < j) h = fmaf(ab[u].x, h, ab[u].y);
+        for (int i = 0; i < kBack; ++i) missing |= ab[i] == kNoAgg;
+        if (!missing || *dead) break;
+        const uint64_t now = globaltimer_ns();
+        if (begin == 0) begin = now;
+        if (now - begin > kWaitNs) {
+            atomicOr(err, kDevTimeout);
+            *dead = true;
+            break;
         }
+        if (h0 == kNoState) h0 = load_word(root);
+#pragma unroll
+        for (int i = 0; i < kBack; ++i)
+            if (ab[i] == kNoAgg) ab[i] = load_word(agg + i * up);
     }
-    if (more && !reset) {
-        C.state[(at + C.strips) * kCh + k] = fmaf(A, h, B);
-        __threadfence();
-        bar_sync(1, kCh);
-        if (k == 0) store_release(C.flag + at, kState);
+    float h = __uint_as_float(h0);
+#pragma unroll
+    for (int i = 0; i < kBack; ++i) {
+        if (i >= J) break;
+        h = run_on(__uint_as_float((uint32_t)ab[i]), h, __uint_as_float((uint32_t)(ab[i] >> 32)));
     }
+    if (more && !reset) publish(C.state + at + up, fmaf(A, h, B));
     return h;
 }
 
-// Sequences without tokens pass their states through.
-__device__ __forceinline__ void pass_empty(const ScanArgs& A, const float* in, float* out) {
-    if (!A.cu || !out) return;
-    for (int n = blockIdx.x; n < A.nseq; n += gridDim.x)
-        if (A.cu[n] == A.cu[n + 1])
-            for (long i = threadIdx.x; i < A.Z * A.d; i += blockDim.x)
-                out[n * A.Z * A.d + i] = in ? in[n * A.Z * A.d + i] : 0.f;
+// One warp's arrival (its earlier shared-memory accesses are done).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+__device__ __forceinline__ void wait_or_give_up(uint64_t* bar, int parity, bool* dead, uint32_t* err) {
+    if (!mbar_wait(bar, parity, *dead ? 0 : kWaitNs)) {
+        if (!*dead && (threadIdx.x & 31) == 0) atomicOr(err, kDevTimeout);
+        *dead = true;
+    }
+}
+
+// 256 compute threads and 128 chain threads share the registers of 384 x 168.
+constexpr int kComputeRegs = 200, kChainRegs = 96;
+static_assert(kComputeRegs * kComputeThreads + kChainRegs * kCh <= 168 * kThreads, "more registers than the block has");
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <typename Tin, bool kShared>
 struct FwdSmem {
     static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
-    static constexpr int kStage = kX + kG;
-    static constexpr int kStages = 2;
-    static constexpr int kRuns = kWarps * kCh * 4;              // one of A, B of all warps
-    static constexpr int kBytes = kStages * kStage + 4 * kRuns + kCh * 4 + 128;
+    static constexpr int kStage = kX + kG, kStages = 3;
+    static constexpr int kRuns = kWarps * kCh;                  // floats of one value of all runs
+    static constexpr int kBytes = kStages * kStage + (4 + 2) * kRuns * 4 + 128;
 };
 
+// The gates of one token: of a channel each, or one for all.
+template <bool kShared>
+struct Gate {
+    P4 v[kRun];
+    __device__ __forceinline__ P4 at(int i) const { return v[i]; }
+    __device__ __forceinline__ void set(int i, const P4& x) { v[i] = x; }
+};
+template <>
+struct Gate<true> {
+    float v[kRun];
+    __device__ __forceinline__ P4 at(int i) const { return all4(v[i]); }
+    __device__ __forceinline__ void set(int i, const P4& x) { v[i] = x.lo.x; }
+};
+template <bool kShared, bool kSlope>
+__device__ __forceinline__ void token_gates(int rule, const float* gt, float gs, P4* a, P4* w, P4* dw) {
+    if constexpr (kShared) {
+        float2 a2, w2, d2 = both(0.f);
+        scan_gates2<kSlope>(rule, both(gs), &a2, &w2, &d2);
+        *a = all4(a2.x);
+        *w = all4(w2.x);
+        *dw = all4(d2.x);
+    } else {
+        const P4 g = ld4(gt);
+        scan_gates2<kSlope>(rule, g.lo, &a->lo, &w->lo, &dw->lo);
+        scan_gates2<kSlope>(rule, g.hi, &a->hi, &w->hi, &dw->hi);
+    }
+}
+
 template <typename Tin, bool kShared>
-__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, Chain C, int tiles) {
+__global__ void __launch_bounds__(kThreads, 1) scan_fwd_kernel(ScanArgs P, Chain C, int tiles) {
     using M = FwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
     float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [2][A, B][warp][128]
-    float* entering = runs + 4 * kWarps * kCh;
-    uint64_t* full = reinterpret_cast<uint64_t*>(entering + kCh);
-    int* window = reinterpret_cast<int*>(full + M::kStages);
+    float* entering = runs + 4 * M::kRuns;                                     // [2][warp][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(entering + 2 * M::kRuns);
+    uint64_t* ready = full + M::kStages;      // a tile's (A, B) of all runs are there
+    uint64_t* entered = ready + 2;            // the states entering them are
     const Strips S(P.Z, P.d);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Tin* x = static_cast<const Tin*>(P.x);
     Tin* o = static_cast<Tin*>(P.o);
     if (threadIdx.x == 0) {
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(ready + i, kWarps), mbar_init(entered + i, kCh / 32);
         fence_mbar_init();
     }
     __syncthreads();
-    pass_empty(P, P.S0, P.S_T);
-    bool dead = false;
-
-    auto prefetch = [&](int tile, int st) {     // by warp 7
-        if (tile >= tiles) return;
+    const int count = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    auto prefetch = [&](int n) {      // by the last warp
+        if (n >= count) return;
+        const int tile = blockIdx.x + n * gridDim.x, st = n % M::kStages;
         const int strip = tile % S.count, t0 = tile / S.count * kTok, rows = min(kTok, P.T - t0);
         if (lane == 0)
             mbar_arrive_expect_tx(full + st, rows * strip_channels(S, P.Z, P.d, strip) * (int)(sizeof(Tin) + (kShared ? 0 : 4)));
@@ -267,136 +342,153 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, Chain
         stage(reinterpret_cast<Tin*>(dst), x, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
         if (!kShared) stage(reinterpret_cast<float*>(dst + M::kX), P.g, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
     };
-    if (warp == kWarps - 1)
-        for (int i = 0; i < M::kStages; ++i) prefetch(blockIdx.x + i * gridDim.x, i);
+    if (warp == kThreads / 32 - 1)
+        for (int i = 0; i < M::kStages; ++i) prefetch(i);
+    begin_chain(P, C, P.S0, P.S_T);
+    bool dead = false;
 
-    int it = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++it) {
-        const int strip = tile % S.count, step = tile / S.count, t0 = step * kTok;
-        const int st = it % M::kStages;
+    if (warp >= kWarps) {             // the chain
+        fewer_registers<kChainRegs>();
+        const int k = threadIdx.x - kComputeThreads;
+        for (int n = 0; n < count; ++n) {
+            const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
+            const ulonglong2 m = chunk_marks(P, C, step);
+            wait_or_give_up(ready + (n & 1), n >> 1 & 1, &dead, P.err);
+            if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);
+            const float* ra = runs + (n & 1) * 2 * M::kRuns + k;
+            float A[kWarps], B[kWarps], tA = 1.f, tB = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                A[w] = ra[w * kCh];
+                B[w] = ra[M::kRuns + w * kCh];
+                tB = run_on(A[w], tB, B[w]);
+                tA *= A[w];
+            }
+            float h = chain_step(C, step, strip, k, tA, tB, m.x != 0, m.x & 1ull, &dead, P.err);
+            float* en = entering + (n & 1) * M::kRuns + k;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                en[w * kCh] = h;
+                h = run_on(A[w], h, B[w]);
+            }
+            warp_arrive(entered + (n & 1));
+        }
+        return;
+    }
+    more_registers<kComputeRegs>();
+
+    struct Set {
+        Gate<kShared> a;
+        P4 b[kRun];
+    };
+    auto reduce = [&](Set& s, int n) {
+        const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
+        const int tw = step * kTok + warp * kRun, st = n % M::kStages;
         const Lane L = lane_of(S, P.Z, P.d, strip, lane);
-        const Marks m = tile_marks(P.cu, P.nseq, P.T, t0);
-        const int tw = t0 + warp * kRun;        // the run's first token
+        const uint32_t first = (uint32_t)(chunk_marks(P, C, step).x >> (warp * kRun)) & ((1u << kRun) - 1u);
+        const bool plain = first == 0 && tw + kRun <= P.T;
         float gs[kRun];
         if (kShared) {
 #pragma unroll
             for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
         }
-        if (!mbar_wait(full + st, (it / M::kStages) & 1, dead ? 0 : kWaitNs)) {
-            if (!dead && lane == 0) atomicOr(P.err, kDevTimeout);
-            dead = true;
-        }
-        // 1. the run's tokens as h = a h' + b, and the run's (A, B)
-        V4 a[kRun], b[kRun], ra = V4{{1.f, 1.f, 1.f, 1.f}}, rb = zero4();
+        wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
         const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + L.smem + warp * kRun * L.row;
         const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + M::kX) + L.smem + warp * kRun * L.row;
+        P4 ra = all4(1.f), rb = all4(0.f);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            a[i] = V4{{1.f, 1.f, 1.f, 1.f}};
-            b[i] = zero4();
-            if (L.on && tw + i < P.T) {
-                const V4 xv = ld4(xs + i * L.row);
-                V4 w;
-                if (kShared) {
-                    scan_gates(P.rule, gs[i], &a[i].v[0], &w.v[0]);
-                    for (int e = 1; e < 4; ++e) a[i].v[e] = a[i].v[0], w.v[e] = w.v[0];
-                } else {
-                    const V4 gv = ld4(gt + i * L.row);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) scan_gates(P.rule, gv.v[e], &a[i].v[e], &w.v[e]);
+            P4 a, w, dw;
+            token_gates<kShared, false>(P.rule, gt + i * L.row, gs[i], &a, &w, &dw);
+            P4 b = mul4(w, ld4(xs + i * L.row));
+            if (!plain) {
+                if (tw + i >= P.T) {             // behind the end: a token that changes nothing
+                    a = all4(1.f);
+                    b = all4(0.f);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) b[i].v[e] = w.v[e] * xv.v[e];
-            }
-            if (m.first >> (warp * kRun + i) & 1u) {      // a sequence begins: its own state enters, no other
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                if (P.S0 && L.on) {
-                    const V4 s0 = ld4(P.S0 + ((long)n * P.Z + L.z) * P.d + L.c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) b[i].v[e] = fmaf(a[i].v[e], s0.v[e], b[i].v[e]);
+                if (first >> i & 1u) {           // a sequence begins: its own state enters, no other
+                    const int q = seq_of(P, tw + i);
+                    if (P.S0 && L.on) b = fma4(a, ld4(P.S0 + ((long)q * P.Z + L.z) * P.d + L.c), b);
+                    a = rb = all4(0.f);
                 }
-                a[i] = zero4();
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ra.v[e] *= a[i].v[e];
-                rb.v[e] = fmaf(a[i].v[e], rb.v[e], b[i].v[e]);
-            }
+            ra = mul4(ra, a);
+            rb = fma4(a, rb, b);
+            s.a.set(i, a);
+            s.b[i] = b;
         }
-        float* runA = runs + (it & 1) * 2 * kWarps * kCh;
-        float* runB = runA + kWarps * kCh;
-        st4(runA + warp * kCh + lane * 4, ra);
-        st4(runB + warp * kCh + lane * 4, rb);
-        __syncthreads();
-        if (warp == kWarps - 1) prefetch(tile + M::kStages * gridDim.x, st);
-        // 2. the state entering the tile
-        if (threadIdx.x < kCh) {
-            const int k = threadIdx.x;
-            float A = 1.f, B = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                B = fmaf(runA[w * kCh + k], B, runB[w * kCh + k]);
-                A *= runA[w * kCh + k];
-            }
-            entering[k] = chain_step(C, step, strip, A, B, m.first != 0, m.first & 1u, &dead, window, P.err);
-        }
-        __syncthreads();
-        // 3. the outputs
-        V4 h = ld4(entering + lane * 4);
-        for (int w = 0; w < warp; ++w) {
-            const V4 pa = ld4(runA + w * kCh + lane * 4), pb = ld4(runB + w * kCh + lane * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h.v[e] = fmaf(pa.v[e], h.v[e], pb.v[e]);
-        }
+        float* out = runs + (n & 1) * 2 * M::kRuns + warp * kCh + lane * 4;
+        if (first) ra = all4(kCut);
+        st4(out, ra);
+        st4(out + M::kRuns, rb);
+        warp_arrive(ready + (n & 1));
+    };
+    auto finish = [&](const Set& s, int n) {
+        const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
+        const int tw = step * kTok + warp * kRun;
+        const Lane L = lane_of(S, P.Z, P.d, strip, lane);
+        const ulonglong2 m = chunk_marks(P, C, step);
+        const uint32_t first = (uint32_t)(m.x >> (warp * kRun)) & ((1u << kRun) - 1u);
+        const uint32_t last = (uint32_t)(m.y >> (warp * kRun)) & ((1u << kRun) - 1u);
+        wait_or_give_up(entered + (n & 1), n >> 1 & 1, &dead, P.err);
+        P4 h = ld4(entering + (n & 1) * M::kRuns + warp * kCh + lane * 4);
+        Tin* out = o ? o + (L.z * P.T + tw) * P.d + L.c : nullptr;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h.v[e] = fmaf(a[i].v[e], h.v[e], b[i].v[e]);
-            if (o && L.on && tw + i < P.T) st4(o + (L.z * P.T + tw + i) * P.d + L.c, h);
-            if (P.S_T && (m.last >> (warp * kRun + i) & 1u)) {
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                if (L.on) st4(P.S_T + ((long)n * P.Z + L.z) * P.d + L.c, h);
-            }
+            if (first >> i & 1u) h = all4(0.f);          // its state is in b
+            h = fma4(s.a.at(i), h, s.b[i]);
+            if (o && L.on && tw + i < P.T) st4(out + i * P.d, h);
+            if (P.S_T && (last >> i & 1u) && L.on) st4(P.S_T + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, h);
         }
+    };
+    Set s0, s1;      // a tile's run waits in one set while the next one is reduced into the other
+    for (int n = 0; n < count; n += 2) {
+        reduce(s0, n);
+        if (n > 0) finish(s1, n - 1);
+        if (n + 1 < count) reduce(s1, n + 1);
+        finish(s0, n);
     }
+    if (count % 2 == 0) finish(s1, count - 1);
 }
 
-// The reverse pass.  c_t = e^{g_t} G_t flows from token t into t - 1 (dS_T into a sequence's last
-// token), G_t = dO_t + c_{t+1}: affine again, c_out = A c_in + R over a run, and the tiles are
-// taken from the last to the first.  A tile's own states are put together again from the state
-// that the forward kept for it, so no state but one of 32 tokens is ever stored.
+// The reverse pass.  c = e^{g_t} G_t flows from token t into t - 1 (dS_T into a sequence's last
+// token), G_t = dO_t + c: affine again, c_out = A c_in + R over a run, and the tiles are taken
+// from the last to the first.  A tile's own states are put together again from the state that
+// the forward kept for it, so no state but one of 64 tokens is ever stored.
 template <typename Tin, bool kShared>
 struct BwdSmem {
     static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
-    static constexpr int kStage = 2 * kX + kG;
-    static constexpr int kStages = 2;
-    static constexpr int kRuns = kWarps * kCh * 4;
-    static constexpr int kBytes = kStages * kStage + 8 * kRuns + kCh * 4 + 128;
+    static constexpr int kStage = 2 * kX + kG, kStages = 2;
+    static constexpr int kRuns = kWarps * kCh;
+    static constexpr int kBytes = kStages * kStage + 6 * kRuns * 4 + 128;
 };
 
 template <typename Tin, bool kShared>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, Chain C, const float* states, float* parts,
+__global__ void __launch_bounds__(kThreads, 1) scan_bwd_kernel(ScanArgs P, Chain C, const float* states, float* parts,
                                                                int tiles) {
     using M = BwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
-    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [2][A, B, Ar, R][warp][128]
-    float* entering = runs + 8 * kWarps * kCh;
-    uint64_t* full = reinterpret_cast<uint64_t*>(entering + kCh);
-    int* window = reinterpret_cast<int*>(full + M::kStages);
+    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [A, B, reverse A, R][warp][128]
+    float* entering = runs + 4 * M::kRuns;                                     // [state, flow][warp][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(entering + 2 * M::kRuns);
+    uint64_t* spent = full + M::kStages;      // a stage has been read to its end
+    uint64_t* ready = spent + M::kStages;
+    uint64_t* entered = ready + 1;
     const Strips S(P.Z, P.d);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Tin* x = static_cast<const Tin*>(P.x);
     const Tin* dO = static_cast<const Tin*>(P.dO);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1), mbar_init(spent + i, kWarps);
+        mbar_init(ready, kWarps);
+        mbar_init(entered, kCh / 32);
         fence_mbar_init();
     }
     __syncthreads();
-    pass_empty(P, P.dST, P.dS0);
-    bool dead = false;
-
-    auto prefetch = [&](int tile, int st) {
-        if (tile >= tiles) return;
+    const int count = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    auto prefetch = [&](int n) {
+        if (n >= count) return;
+        const int tile = blockIdx.x + n * gridDim.x, st = n % M::kStages;
         const int strip = tile % S.count, t0 = (C.steps - 1 - tile / S.count) * kTok, rows = min(kTok, P.T - t0);
         if (lane == 0)
             mbar_arrive_expect_tx(full + st,
@@ -407,173 +499,159 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, Chain
         stage(reinterpret_cast<Tin*>(dst + M::kX), dO, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
         if (!kShared) stage(reinterpret_cast<float*>(dst + 2 * M::kX), P.g, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
     };
-    if (warp == kWarps - 1)
-        for (int i = 0; i < M::kStages; ++i) prefetch(blockIdx.x + i * gridDim.x, i);
+    if (warp == kThreads / 32 - 1)
+        for (int i = 0; i < M::kStages; ++i) prefetch(i);
+    begin_chain(P, C, P.dST, P.dS0);
+    bool dead = false;
 
-    int it = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++it) {
-        const int strip = tile % S.count, step = tile / S.count, chunk = C.steps - 1 - step, t0 = chunk * kTok;
-        const int st = it % M::kStages;
+    if (warp >= kWarps) {             // the chain
+        fewer_registers<kChainRegs>();
+        const int k = threadIdx.x - kComputeThreads;
+        for (int n = 0; n < count; ++n) {
+            const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
+            const int chunk = C.steps - 1 - step;
+            const ulonglong2 m = chunk_marks(P, C, chunk);
+            float h = m.x & 1ull ? 0.f : states[((size_t)chunk * S.count + strip) * kCh + k];
+            wait_or_give_up(ready, n & 1, &dead, P.err);
+            float A[kWarps], B[kWarps], tA = 1.f, tB = 0.f;
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) {
+                A[w] = runs[2 * M::kRuns + w * kCh + k];
+                B[w] = runs[3 * M::kRuns + w * kCh + k];
+                tB = run_on(A[w], tB, B[w]);
+                tA *= A[w];
+            }
+            const bool at_end = P.T - chunk * kTok <= kTok || (m.y >> (kTok - 1) & 1ull);     // nothing flows in
+            float c = chain_step(C, step, strip, k, tA, tB, m.y != 0, at_end, &dead, P.err);
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) {
+                entering[M::kRuns + w * kCh + k] = c;
+                c = run_on(A[w], c, B[w]);
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                entering[w * kCh + k] = h;
+                h = run_on(runs[w * kCh + k], h, runs[M::kRuns + w * kCh + k]);
+            }
+            warp_arrive(entered);
+            if (warp == kThreads / 32 - 1 && n + M::kStages < count) {
+                wait_or_give_up(spent + n % M::kStages, n / M::kStages & 1, &dead, P.err);
+                prefetch(n + M::kStages);
+            }
+        }
+        return;
+    }
+    more_registers<kComputeRegs>();
+
+    for (int n = 0; n < count; ++n) {
+        const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
+        const int chunk = C.steps - 1 - step, tw = chunk * kTok + warp * kRun, st = n % M::kStages;
         const Lane L = lane_of(S, P.Z, P.d, strip, lane);
-        const Marks m = tile_marks(P.cu, P.nseq, P.T, t0);
-        const int tw = t0 + warp * kRun;
+        const ulonglong2 m = chunk_marks(P, C, chunk);
+        const uint32_t first = (uint32_t)(m.x >> (warp * kRun)) & ((1u << kRun) - 1u);
+        const uint32_t last = (uint32_t)(m.y >> (warp * kRun)) & ((1u << kRun) - 1u);
+        const bool plain = (first | last) == 0 && tw + kRun <= P.T;
         float gs[kRun];
         if (kShared) {
 #pragma unroll
             for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
         }
-        V4 h = m.first & 1u ? zero4() : ld4(states + ((size_t)chunk * S.count + strip) * kCh + lane * 4);
-        if (!mbar_wait(full + st, (it / M::kStages) & 1, dead ? 0 : kWaitNs)) {
-            if (!dead && lane == 0) atomicOr(P.err, kDevTimeout);
-            dead = true;
-        }
-        // 1. the run's tokens: a, w, b = w x, e = w' x, u = dO; the forward's and the reverse's (A, B)
-        V4 a[kRun], w[kShared ? 1 : kRun], b[kRun], e[kRun], u[kRun];
-        float ws[kRun];
-        V4 ra = V4{{1.f, 1.f, 1.f, 1.f}}, rb = zero4();
-        const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + L.smem + warp * kRun * L.row;
-        const Tin* us = reinterpret_cast<const Tin*>(smem + st * M::kStage + M::kX) + L.smem + warp * kRun * L.row;
-        const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + 2 * M::kX) + L.smem + warp * kRun * L.row;
-        V4 s0 = zero4();          // the state of the last sequence that begins in the run
+        wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
+        const int off = L.smem + warp * kRun * L.row;
+        const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + off;
+        const Tin* us = reinterpret_cast<const Tin*>(smem + st * M::kStage + M::kX) + off;
+        const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + 2 * M::kX) + off;
+        auto state0 = [&](const float* from, int t) {      // a sequence's row of S0 or dS_T
+            return from && L.on ? ld4(from + ((long)seq_of(P, t) * P.Z + L.z) * P.d + L.c) : all4(0.f);
+        };
+        // 1. the gates, and the run's (A, B) forward and in reverse
+        Gate<kShared> a, w, dw;
+        P4 ra = all4(1.f), rb = all4(0.f);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            a[i] = V4{{1.f, 1.f, 1.f, 1.f}};
-            b[i] = e[i] = u[i] = zero4();
-            ws[i] = 0.f;
-            if (!kShared) w[i] = zero4();
-            if (L.on && tw + i < P.T) {
-                const V4 xv = ld4(xs + i * L.row);
-                u[i] = ld4(us + i * L.row);
-                if (kShared) {
-                    float dw;
-                    scan_gates(P.rule, gs[i], &a[i].v[0], &ws[i], &dw);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[i].v[j] = a[i].v[0];
-                        b[i].v[j] = ws[i] * xv.v[j];
-                        e[i].v[j] = dw * xv.v[j];
-                    }
-                } else {
-                    const V4 gv = ld4(gt + i * L.row);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float dw;
-                        scan_gates(P.rule, gv.v[j], &a[i].v[j], &w[i].v[j], &dw);
-                        b[i].v[j] = w[i].v[j] * xv.v[j];
-                        e[i].v[j] = dw * xv.v[j];
-                    }
+            P4 a1, w1, dw1;
+            token_gates<kShared, true>(P.rule, gt + i * L.row, gs[i], &a1, &w1, &dw1);
+            if (!plain) {
+                if (tw + i >= P.T) {
+                    a1 = all4(1.f);
+                    w1 = dw1 = all4(0.f);
+                }
+                if (first >> i & 1u) {
+                    ra = all4(0.f);
+                    rb = state0(P.S0, tw + i);
                 }
             }
-            const bool first = m.first >> (warp * kRun + i) & 1u;
-            if (first) {
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                s0 = P.S0 && L.on ? ld4(P.S0 + ((long)n * P.Z + L.z) * P.d + L.c) : zero4();
-                ra = zero4();
-                rb = s0;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ra.v[j] *= a[i].v[j];
-                rb.v[j] = fmaf(a[i].v[j], rb.v[j], b[i].v[j]);
-            }
+            ra = mul4(ra, a1);
+            P4 b = mul4(w1, ld4(xs + i * L.row));
+            if (!plain && tw + i >= P.T) b = all4(0.f);     // the stage holds anything there
+            rb = fma4(a1, rb, b);
+            a.set(i, a1);
+            w.set(i, w1);
+            dw.set(i, dw1);
         }
-        float* runA = runs + (it & 1) * 4 * kWarps * kCh;
-        float* runB = runA + kWarps * kCh;
-        float* revA = runB + kWarps * kCh;
-        float* revB = revA + kWarps * kCh;
-        st4(runA + warp * kCh + lane * 4, ra);
-        st4(runB + warp * kCh + lane * 4, rb);
-        ra = V4{{1.f, 1.f, 1.f, 1.f}};
-        rb = zero4();
+        float* out = runs + warp * kCh + lane * 4;
+        if (first) ra = all4(kCut);
+        st4(out, ra);
+        st4(out + M::kRuns, rb);
+        ra = all4(1.f);
+        rb = all4(0.f);
 #pragma unroll
         for (int i = kRun - 1; i >= 0; --i) {
-            if (m.last >> (warp * kRun + i) & 1u) {
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                ra = zero4();
-                rb = P.dST && L.on ? ld4(P.dST + ((long)n * P.Z + L.z) * P.d + L.c) : zero4();
+            P4 u = ld4(us + i * L.row);
+            if (!plain) {
+                if (tw + i >= P.T) u = all4(0.f);
+                if (last >> i & 1u) {
+                    ra = all4(0.f);
+                    rb = state0(P.dST, tw + i);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ra.v[j] *= a[i].v[j];
-                rb.v[j] = a[i].v[j] * (u[i].v[j] + rb.v[j]);
-            }
+            ra = mul4(ra, a.at(i));
+            rb = mul4(a.at(i), add4(u, rb));
         }
-        st4(revA + warp * kCh + lane * 4, ra);
-        st4(revB + warp * kCh + lane * 4, rb);
-        __syncthreads();
-        if (warp == kWarps - 1) prefetch(tile + M::kStages * gridDim.x, st);
-        // 2. what flows into the tile from behind
-        if (threadIdx.x < kCh) {
-            const int k = threadIdx.x;
-            float A = 1.f, B = 0.f;
-#pragma unroll
-            for (int q = kWarps - 1; q >= 0; --q) {
-                B = fmaf(revA[q * kCh + k], B, revB[q * kCh + k]);
-                A *= revA[q * kCh + k];
-            }
-            const bool at_end = t0 + kTok >= P.T || (m.last >> (kTok - 1) & 1u);   // nothing flows in
-            entering[k] = chain_step(C, step, strip, A, B, m.last != 0, at_end, &dead, window, P.err);
-        }
-        // 3. the states before the run's tokens: e becomes a h' + w' x
-        for (int q = 0; q < warp; ++q) {
-            const V4 pa = ld4(runA + q * kCh + lane * 4), pb = ld4(runB + q * kCh + lane * 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h.v[j] = fmaf(pa.v[j], h.v[j], pb.v[j]);
-        }
+        if (last) ra = all4(kCut);
+        st4(out + 2 * M::kRuns, ra);
+        st4(out + 3 * M::kRuns, rb);
+        warp_arrive(ready);
+        wait_or_give_up(entered, n & 1, &dead, P.err);
+        // 2. the states before the run's tokens: e = a h' + w' x
+        P4 e[kRun];
+        P4 h = ld4(entering + warp * kCh + lane * 4);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            if (m.first >> (warp * kRun + i) & 1u) {
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                h = P.S0 && L.on ? ld4(P.S0 + ((long)n * P.Z + L.z) * P.d + L.c) : zero4();
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float ah = a[i].v[j] * h.v[j];
-                e[i].v[j] += ah;
-                h.v[j] = ah + b[i].v[j];
-            }
+            if (!plain && (first >> i & 1u)) h = state0(P.S0, tw + i);
+            const P4 xv = ld4(xs + i * L.row);
+            e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
+            h = fma4(a.at(i), h, mul4(w.at(i), xv));
         }
-        __syncthreads();
-        // 4. the gradients
-        V4 c = ld4(entering + lane * 4);
-        for (int q = kWarps - 1; q > warp; --q) {
-            const V4 pa = ld4(revA + q * kCh + lane * 4), pb = ld4(revB + q * kCh + lane * 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c.v[j] = fmaf(pa.v[j], c.v[j], pb.v[j]);
-        }
+        // 3. the gradients
+        P4 c = ld4(entering + M::kRuns + warp * kCh + lane * 4);
+        float* dx = P.dx + (L.z * P.T + tw) * P.d + L.c;
+        float* dg = P.dg + (L.z * P.T + tw) * (kShared ? 1 : P.d) + (kShared ? 0 : L.c);
 #pragma unroll
         for (int i = kRun - 1; i >= 0; --i) {
-            const int t = tw + i;
-            if (m.last >> (warp * kRun + i) & 1u) {
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                c = P.dST && L.on ? ld4(P.dST + ((long)n * P.Z + L.z) * P.d + L.c) : zero4();
-            }
-            V4 dx, dg;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float G = u[i].v[j] + c.v[j];
-                dx.v[j] = (kShared ? ws[i] : w[kShared ? 0 : i].v[j]) * G;
-                dg.v[j] = G * e[i].v[j];
-                c.v[j] = a[i].v[j] * G;
-            }
-            const bool live = L.on && t < P.T;
+            const bool live = L.on && tw + i < P.T;
+            if (!plain && (last >> i & 1u)) c = state0(P.dST, tw + i);
+            const P4 G = add4(ld4(us + i * L.row), c);
+            const P4 dgv = mul4(e[i], G);
+            c = mul4(a.at(i), G);
+            if (!plain && tw + i >= P.T) c = all4(0.f);      // behind the end; the last token's own comes next
             if (live) {
-                st4(P.dx + (L.z * P.T + t) * P.d + L.c, dx);
-                if (!kShared) st4(P.dg + (L.z * P.T + t) * P.d + L.c, dg);
+                st4(dx + i * P.d, mul4(w.at(i), G));
+                if (!kShared) st4(dg + i * P.d, dgv);
             }
             if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
-                float sum = live ? (dg.v[0] + dg.v[1]) + (dg.v[2] + dg.v[3]) : 0.f;
-                for (int off = S.heads > 1 ? S.dv / 2 : 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                float sum = live ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
+                for (int far = S.heads > 1 ? S.dv / 2 : 16; far > 0; far >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, far);
                 if (live && (S.heads > 1 ? lane % S.dv == 0 : lane == 0)) {
-                    if (S.per_head == 1) P.dg[L.z * P.T + t] = sum;
-                    else parts[((long)(strip % S.per_head) * P.Z + L.z) * P.T + t] = sum;
+                    if (S.per_head == 1) dg[i] = sum;
+                    else parts[((long)(strip % S.per_head) * P.Z + L.z) * P.T + tw + i] = sum;
                 }
             }
-            if (P.dS0 && (m.first >> (warp * kRun + i) & 1u)) {
-                const int n = __shfl_sync(0xffffffffu, m.n, warp * kRun + i);
-                if (L.on) st4(P.dS0 + ((long)n * P.Z + L.z) * P.d + L.c, c);
-            }
+            if (!plain && P.dS0 && (first >> i & 1u) && L.on)
+                st4(P.dS0 + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, c);
         }
+        warp_arrive(spent + st);
     }
 }
 
@@ -603,17 +681,10 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Tin* __restrict__ 
         from = p.read < 0 ? nullptr : reinterpret_cast<float*>(reinterpret_cast<char*>(S) + p.read * P.page_bytes);
     }
     if (j >= H * d) return;
-    const V4 xv = ld4(x + row + j);
-    V4 gv;
-    if (gw == 1) gv.v[0] = gv.v[1] = gv.v[2] = gv.v[3] = g[(long)n * H + j / d];
-    else gv = ld4(g + row + j);
-    V4 h = from ? ld4(from + j) : zero4();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, w;
-        scan_gates(rule, gv.v[i], &a, &w);
-        h.v[i] = fmaf(a, h.v[i], w * xv.v[i]);
-    }
+    P4 a, w, dw;
+    if (gw == 1) token_gates<true, false>(rule, nullptr, g[(long)n * H + j / d], &a, &w, &dw);
+    else token_gates<false, false>(rule, g + row + j, 0.f, &a, &w, &dw);
+    const P4 h = fma4(a, from ? ld4(from + j) : all4(0.f), mul4(w, ld4(x + row + j)));
     st4(to + j, h);
     st4(o + row + j, h);
 }
@@ -623,17 +694,15 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Tin* __restrict__ 
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 static long scan_steps(int T) { return ((long)T + kTok - 1) / kTok; }
 
-size_t scan_states_bytes(long Z, int T, int d) {
-    return up256((size_t)scan_steps(T) * Strips(Z, d).count * kCh * sizeof(float));
-}
-// flags and (A, B) of every tile; backward: also the flows between tiles, and the partial sums of
-// a shared decay's gradient where a head is wider than a strip
+size_t scan_states_bytes(long Z, int T, int d) { return (size_t)scan_steps(T) * Strips(Z, d).count * kCh * sizeof(float); }
+// (A, B) of every tile and the chunks' marks; backward: also the flows between tiles, and the
+// partial sums of a shared decay's gradient where a head is wider than a strip
 size_t scan_scratch_bytes(long Z, int T, int d, int gw, bool backward) {
     const Strips S(Z, d);
     const size_t tiles = (size_t)scan_steps(T) * S.count;
-    size_t n = up256(tiles * sizeof(int)) + tiles * kCh * sizeof(float2);
+    size_t n = tiles * kCh * sizeof(unsigned long long) + up256(scan_steps(T) * sizeof(ulonglong2));
     if (backward) {
-        n += up256(tiles * kCh * sizeof(float));
+        n += tiles * kCh * sizeof(float);
         if (gw == 1 && S.per_head > 1) n += up256((size_t)S.per_head * Z * T * sizeof(float));
     }
     return n;
@@ -641,9 +710,9 @@ size_t scan_scratch_bytes(long Z, int T, int d, int gw, bool backward) {
 
 namespace {
 
-// Launches with every block resident at once (at most one per tile), after clearing the flags.
+// Launches with every block resident at once, at most one per tile.
 template <typename Kernel, typename... Args>
-cudaError_t launch_tiles(Kernel kernel, int smem, std::atomic<int>* resident, const Chain& C, long tiles,
+cudaError_t launch_tiles(Kernel kernel, int smem, std::atomic<int>* resident, bool waits, long tiles,
                          cudaStream_t stream, Args... args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -653,13 +722,14 @@ cudaError_t launch_tiles(Kernel kernel, int smem, std::atomic<int>* resident, co
         int sms = 0, per = 0;
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        // the register split of compute and chain warps fits what the block is launched with
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+        if (fa.numRegs * kThreads < kComputeRegs * kComputeThreads + kChainRegs * kCh) return cudaErrorInvalidConfiguration;
         if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem)) != cudaSuccess) return e;
         most = sms * per;
         if (dev < 64) resident[dev].store(most, std::memory_order_relaxed);
     }
-    if (C.steps > 1 &&
-        (e = cudaMemsetAsync(C.flag, 0, (size_t)C.steps * C.strips * sizeof(int), stream)) != cudaSuccess)
-        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles < most ? tiles : most));
     cfg.blockDim = dim3(kThreads);
@@ -669,19 +739,19 @@ cudaError_t launch_tiles(Kernel kernel, int smem, std::atomic<int>* resident, co
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = C.steps > 1 ? 1 : 0;      // blocks wait for one another only across steps
+    cfg.numAttrs = waits ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 Chain scan_chain(const ScanArgs& a, float* states, long* tiles) {
-    const Strips S(a.Z, a.d);
     Chain C;
-    C.strips = S.count;
+    C.strips = Strips(a.Z, a.d).count;
     C.steps = (int)scan_steps(a.T);
     *tiles = (long)C.steps * C.strips;
-    C.flag = static_cast<int*>(a.scratch);
-    C.agg = reinterpret_cast<float2*>(static_cast<char*>(a.scratch) + up256((size_t)*tiles * sizeof(int)));
-    C.state = states ? states : reinterpret_cast<float*>(C.agg + (size_t)*tiles * kCh);
+    C.agg = static_cast<unsigned long long*>(a.scratch);
+    C.marks = reinterpret_cast<ulonglong2*>(C.agg + (size_t)*tiles * kCh);
+    C.state = states ? states
+                     : reinterpret_cast<float*>(reinterpret_cast<char*>(C.marks) + up256(C.steps * sizeof(ulonglong2)));
     return C;
 }
 
@@ -691,8 +761,8 @@ cudaError_t launch_fwd(const ScanArgs& a, cudaStream_t stream) {
     long tiles;
     const Chain C = scan_chain(a, a.E, &tiles);
     if (tiles >= (1l << 31)) return cudaErrorInvalidValue;
-    return launch_tiles(scan_fwd_kernel<Tin, kShared>, FwdSmem<Tin, kShared>::kBytes, resident, C, tiles, stream, a, C,
-                        (int)tiles);
+    return launch_tiles(scan_fwd_kernel<Tin, kShared>, FwdSmem<Tin, kShared>::kBytes, resident, C.steps > 1 || a.cu, tiles,
+                        stream, a, C, (int)tiles);
 }
 
 template <typename Tin, bool kShared>
@@ -702,9 +772,9 @@ cudaError_t launch_bwd(const ScanArgs& a, cudaStream_t stream) {
     const Chain C = scan_chain(a, nullptr, &tiles);
     if (tiles >= (1l << 31)) return cudaErrorInvalidValue;
     const int per_head = Strips(a.Z, a.d).per_head;
-    float* parts = reinterpret_cast<float*>(reinterpret_cast<char*>(C.state) + up256((size_t)tiles * kCh * sizeof(float)));
-    cudaError_t e = launch_tiles(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::kBytes, resident, C, tiles, stream,
-                                 a, C, (const float*)a.E, parts, (int)tiles);
+    float* parts = C.state + (size_t)tiles * kCh;
+    cudaError_t e = launch_tiles(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::kBytes, resident,
+                                 C.steps > 1 || a.cu, tiles, stream, a, C, (const float*)a.E, parts, (int)tiles);
     if (e != cudaSuccess || !kShared || per_head == 1) return e;
     const long n = a.Z * a.T, blocks = (n + 255) / 256;
     scan_parts_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(parts, a.dg, n, per_head);

@@ -13,49 +13,78 @@
 
 namespace efla {
 
-// a = e^g, w = phi(g) and, for the backward pass, w' = phi'(g) in fp32.
-// For |g| < 1/2 all three come from v(g) = (phi(g) - 1) / g = sum_n g^n / (n + 2)!, cut after
-// g^6 / 8! (the rest is below g^7 / 9! < 2.2e-8): w = 1 + g v and, from phi' = (e^g - phi) / g
-// with e^g = 1 + g phi, w' = w - v, which has no cancellation near 0.  Elsewhere w = (a - 1) / g
-// and w' = (a - w) / g by their definitions (|a - 1| >= 0.39 and |a - w| >= 0.18: few digits
-// cancel, and none for long decays).
+// Pairs of fp32 in one instruction (the FMA pipe takes two per lane and issue).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a = e^g, w = phi(g) and, for the backward pass, w' = phi'(g) in fp32, two at a time.
+// For |g| < 1 all come from v(g) = (phi(g) - 1) / g = sum_n g^n / (n + 2)!, cut after g^8 / 10!
+// (the rest is below 1 / 11! = 2.5e-8): w = 1 + g v, a = 1 + g w, and from phi' = (a - w) / g,
+// w' = w - v.  Nothing cancels near 0, and a long memory's a is as good as its rounding.
+// Elsewhere a is 2^(g log2 e), w = (a - 1) / g and w' = (a - w) / g by their definitions
+// (|a - 1| >= 0.63, |a - w| >= 0.26); a's error there, up to (4 + |g|) 2^-24 relative, belongs to a
+// memory of a token or two.  With u = 2^-24: a below 5 u, w below 6 u, w' below 24 u.
 // g = -inf gives a = w = w' = 0: the token forgets everything and writes nothing.
-__device__ __forceinline__ float scan_v(float g) {
-    float v = 1.0f / 40320.0f;
-    v = fmaf(v, g, 1.0f / 5040.0f);
-    v = fmaf(v, g, 1.0f / 720.0f);
-    v = fmaf(v, g, 1.0f / 120.0f);
-    v = fmaf(v, g, 1.0f / 24.0f);
-    v = fmaf(v, g, 1.0f / 6.0f);
-    return fmaf(v, g, 0.5f);
-}
-__device__ __forceinline__ void scan_gates(int rule, float g, float* a, float* w) {
-    *a = expf(g);
-    if (rule == kRuleEuler) {
-        *w = 1.0f;
-        return;
+template <bool kSlope>
+__device__ __forceinline__ void scan_gates2(int rule, float2 g, float2* a, float2* w, float2* dw) {
+    float2 v = both(1.0f / 3628800.0f);
+    v = fma2(v, g, both(1.0f / 362880.0f));
+    v = fma2(v, g, both(1.0f / 40320.0f));
+    v = fma2(v, g, both(1.0f / 5040.0f));
+    v = fma2(v, g, both(1.0f / 720.0f));
+    v = fma2(v, g, both(1.0f / 120.0f));
+    v = fma2(v, g, both(1.0f / 24.0f));
+    v = fma2(v, g, both(1.0f / 6.0f));
+    v = fma2(v, g, both(0.5f));
+    const float2 w0 = fma2(g, v, both(1.0f)), a0 = fma2(g, w0, both(1.0f));
+    const float2 t = mul2(g, both(1.44269504f)), r = make_float2(fast_rcp(g.x), fast_rcp(g.y));
+    const float2 a1 = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+    const float2 w1 = mul2(add2(a1, both(-1.0f)), r);
+    const bool sx = fabsf(g.x) < 1.0f, sy = fabsf(g.y) < 1.0f;
+    *a = make_float2(sx ? a0.x : a1.x, sy ? a0.y : a1.y);
+    *w = make_float2(sx ? w0.x : w1.x, sy ? w0.y : w1.y);
+    if constexpr (kSlope) {
+        const float2 d0 = fma2(v, both(-1.0f), w0), d1 = mul2(fma2(w1, both(-1.0f), a1), r);
+        *dw = make_float2(sx ? d0.x : d1.x, sy ? d0.y : d1.y);
+        if (rule == kRuleEuler) *dw = both(0.0f);
     }
-    const float near0 = fmaf(g, scan_v(g), 1.0f);
-    const float far = __fdividef(*a - 1.0f, g);
-    *w = fabsf(g) < 0.5f ? near0 : far;
-}
-__device__ __forceinline__ void scan_gates(int rule, float g, float* a, float* w, float* dw) {
-    *a = expf(g);
-    if (rule == kRuleEuler) {
-        *w = 1.0f;
-        *dw = 0.0f;
-        return;
-    }
-    const bool small = fabsf(g) < 0.5f;
-    const float v = scan_v(g), near0 = fmaf(g, v, 1.0f);
-    const float far = __fdividef(*a - 1.0f, g);
-    *w = small ? near0 : far;
-    *dw = small ? near0 - v : __fdividef(*a - far, g);
+    if (rule == kRuleEuler) *w = both(1.0f);
 }
 
 // Streams [Z][T][d] (dense: Z = B*H, one sequence each; packed: Z = H, sequences cu[n] ..
 // cu[n+1] of every stream); states [(n * Z + z) * d], n = 0 for dense batches.
-constexpr int kScanChunk = 32;      // tokens between two saved states
+constexpr int kScanChunk = 64;      // tokens between two saved states
 struct ScanArgs {
     const void* x = nullptr;
     const float* g = nullptr;       // [Z][T][gw], gw = d or 1
@@ -66,7 +95,7 @@ struct ScanArgs {
     const float* S0 = nullptr;
     void* o = nullptr;              // forward; null: states only
     float* S_T = nullptr;
-    float* E = nullptr;             // [ceil(T / 32)][Z][d]: the state before token 32 c (written by the forward)
+    float* E = nullptr;             // the state before token 64 c, by strips (written by the forward)
     // backward
     const void* dO = nullptr;
     const float* dST = nullptr;

@@ -175,6 +175,24 @@ def test_non_finite_inputs_stay_in_their_channel(efla, cuda):
     assert torch.equal(got["o"][:, :, :40], clean["o"][:, :, :40])
 
 
+@pytest.mark.parametrize("per_channel", [True, False])
+def test_packed_sequences_do_not_touch_each_other(efla, cuda, per_channel):
+    """NaN and infinities of one sequence stay in it, forward and back, wherever its ends lie in the tiles."""
+    cu = offsets([70, 5, 3, 1, 90, 64, 128, 30, 300, 2])
+    inp = inputs(10, 2, cu[-1], 64, torch.float32, per_channel, cu=cu)
+    clean = run_both(efla, inp, cu)
+    for n in (0, 2, 4, 6, 8):
+        for name in ("x", "dO"):
+            inp[name][:, cu[n]:cu[n + 1]] = float("nan")
+        inp["S0"][n], inp["dS_T"][n] = float("inf"), float("nan")
+    got = run_both(efla, inp, cu)
+    for n in (1, 3, 5, 7, 9):
+        for name in ("o", "dx", "dg"):
+            assert torch.equal(got[name][:, cu[n]:cu[n + 1]], clean[name][:, cu[n]:cu[n + 1]]), (n, name)
+        assert torch.equal(got["S_T"][n], clean["S_T"][n]) and torch.equal(got["dS0"][n], clean["dS0"][n])
+    assert torch.isnan(got["o"][:, cu[4]:cu[5]]).all() and torch.isnan(got["dx"][:, cu[4]:cu[5]]).all()
+
+
 def test_backward_against_differences(efla, cuda):
     """The loss's directional derivatives by central differences of the fp64 forward."""
     inp = inputs(1, 2, 70, 16, torch.float32, True, seed=2)
