@@ -1,24 +1,17 @@
 // efla_scan.cu -- the per-channel gated linear recurrence: forward, backward, one token.
 //
 // The recurrence is affine in the state: over any run of tokens h_out = A h_in + B, and runs
-// compose.  A tile is 64 tokens x 128 channels (a "strip"); its eight compute warps take eight
-// tokens each, a lane four channels.  Per tile:
-//   1. every compute thread reduces its run to (A, B), which goes to shared memory;
-//   2. the chain warps (a thread per channel) publish the tile's (A, B), put the state entering
-//      the tile together from the preceding tiles of the strip (look back: the state that entered
-//      a tile some steps before and the (A, B) since, in token order), publish the state leaving
-//      the tile, and hand every run the state entering it;
-//   3. every compute thread continues its run from there and writes the outputs.
-// Inputs are staged by bulk copies some tiles ahead, and are read from memory once.
-//
-// What is published is its own signal: a word that is not there yet holds a bit pattern that no
-// result has (all ones), so publishing takes one store and reading it one load, without fences
-// or flags.  The state leaving a tile is always fma(A, entering, B) of the same numbers, wherever
-// the look back started, so results do not depend on timing.  The grid is launched cooperatively:
-// all blocks are resident and take tiles in time order (block b: tiles b, b + grid, ...), so
-// every wait is for a tile that a running block has begun or finished; each wait is bounded.
-#include <cooperative_groups.h>
-
+// compose.  A tile is 32 tokens x 128 channels (a "strip").  A cluster of blocks takes one strip
+// along time: in each turn its blocks hold consecutive tiles, and
+//   1. the eight compute warps reduce four tokens each (a lane holds four channels) to (A, B);
+//   2. the two chain warps (a thread holds two channels) fold these to the tile's (A, B), write it
+//      into the shared memory of every block of the cluster, and fold what all blocks sent onto
+//      the state the turn began with: the state entering the block's own tile, the one entering
+//      each of its runs, and the one that the next turn begins with, which is thus known to every
+//      block without another exchange;
+//   3. the compute warps continue their runs from there and write the outputs.
+// Inputs are staged by bulk copies some turns ahead and read from memory once.  Everything is
+// folded in token order, so the results are the same bits on every run.
 #include "efla_kernels.h"
 #include "efla_pages.cuh"
 #include "efla_scan.cuh"
@@ -48,9 +41,10 @@ __device__ __forceinline__ void st4(T* p, const P4& v) {
 }
 
 constexpr int kTok = kScanChunk, kWarps = 8, kRun = kTok / kWarps, kCh = 128;
-constexpr int kComputeThreads = kWarps * 32, kThreads = kComputeThreads + kCh;
+constexpr int kComputeThreads = kWarps * 32, kChainThreads = kCh / 2, kThreads = kComputeThreads + kChainThreads;
+constexpr int kCluster = 16;       // most blocks of a cluster
+constexpr int kMarks = 8;          // chunks whose marks are kept
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kBack = 16;          // most (A, B) that one look back folds
 
 // How lanes map to (stream, channel): heads of d channels with 32 % (d / 4) == 0 are packed
 // side by side into a strip; other widths up to 128 take a strip each, wider ones several.
@@ -67,32 +61,35 @@ struct Strips {
     }
 };
 
+// What a lane holds of any strip.
 struct Lane {
-    long z;
-    int c;           // first channel
-    bool on;
-    int smem;        // element offset of token 0 in a staged tile
-    int row;         // elements between tokens there
-};
-__device__ __forceinline__ Lane lane_of(const Strips& S, long Z, int d, int strip, int lane) {
-    Lane L;
-    if (S.heads > 1) {
-        const int p = lane / S.dv;
-        L.z = (long)strip * S.heads + p;
-        L.c = (lane % S.dv) * 4;
-        L.on = L.z < Z;
-        L.smem = p * kTok * d + L.c;
-        L.row = d;
-    } else {
-        const int part = strip % S.per_head;
-        L.z = strip / S.per_head;
-        L.c = (part * 32 + lane) * 4;
-        L.on = L.c < d;
-        L.smem = lane * 4;
-        L.row = S.per_head > 1 ? kCh : d;
-        if (!L.on) L.smem = 0;       // read something that is there, use nothing of it
+    int c, smem, row;     // channel within the head or its part; offset of token 0 in a staged tile; elements between tokens
+    int p, heads, per_head, d;
+    long Z;
+    __device__ __forceinline__ Lane(const Strips& S, long Z_, int d_, int lane)
+        : heads(S.heads), per_head(S.per_head), d(d_), Z(Z_) {
+        p = S.heads > 1 ? lane / S.dv : 0;
+        c = S.heads > 1 ? (lane % S.dv) * 4 : lane * 4;
+        row = S.per_head > 1 ? kCh : d_;
+        smem = S.heads > 1 ? p * kTok * d_ + c : c < row ? c : 0;       // off lanes: something that is there
     }
-    return L;
+};
+struct Spot {
+    long z;
+    int c;
+    bool on;
+};
+__device__ __forceinline__ Spot spot_of(const Lane& L, int strip) {
+    Spot s;
+    if (L.per_head == 1) {
+        s.z = (long)strip * L.heads + L.p;
+        s.c = L.c;
+    } else {
+        s.z = strip / L.per_head;
+        s.c = (strip % L.per_head) * kCh + L.c;
+    }
+    s.on = s.z < L.Z && s.c < L.d;
+    return s;
 }
 
 // Stage one tensor's tile (one warp calls it; the barrier already expects the bytes).  A strip
@@ -130,129 +127,70 @@ __device__ __forceinline__ int seq_of(const ScanArgs& P, int t) {
     return lo;
 }
 
-// What the tiles of a strip publish, by step (chunk in the direction of the recurrence) and strip,
-// and which of a chunk's tokens begin or end a sequence (bit l: token l; packed batches).
-struct Chain {
-    unsigned long long* agg;     // [steps][strips][128]: A, B
-    float* state;                // [steps][strips][128]: entering
-    ulonglong2* marks;           // [chunks]: first, last
-    int strips, steps;
-};
-constexpr unsigned long long kNoAgg = ~0ull;
-constexpr uint32_t kNoState = ~0u;
+// Which of a chunk's tokens begin or end a sequence (bit l: token l).  One warp calls it.
+__device__ __forceinline__ uint2 chunk_marks(const ScanArgs& P, int chunk) {
+    const int t0 = chunk * kTok;
+    if (!P.cu) return make_uint2(chunk == 0 ? 1u : 0u, P.T - t0 <= kTok ? 1u << (P.T - t0 - 1) : 0u);
+    static_assert(kTok == 32, "one lane per token");
+    const int t = t0 + (threadIdx.x & 31), n = t < P.T ? seq_of(P, t) : 0;
+    return make_uint2(__ballot_sync(0xffffffffu, t < P.T && P.cu[n] == t),
+                      __ballot_sync(0xffffffffu, t < P.T && P.cu[n + 1] == t + 1));
+}
+__device__ __forceinline__ uint32_t run_bits(uint32_t marks, int warp) {
+    return marks >> (warp * kRun) & ((1u << kRun) - 1u);
+}
+
+// Sequences without tokens pass their states through.
+__device__ __forceinline__ void pass_empty(const ScanArgs& P, const float* in, float* out) {
+    if (!P.cu || !out) return;
+    for (int n = blockIdx.x; n < P.nseq; n += gridDim.x)
+        if (P.cu[n] == P.cu[n + 1])
+            for (long i = threadIdx.x; i < P.Z * P.d; i += kThreads)
+                out[n * P.Z * P.d + i] = in ? in[n * P.Z * P.d + i] : 0.f;
+}
+
 // A of a run with a sequence's begin in it: what came before does not matter, not even a NaN.
-// (No product of decays is -0.)
+// (No product of decays is -0.)  A cut is one for all channels.
 constexpr float kCut = -0.0f;
-__device__ __forceinline__ float run_on(float A, float h, float B) {
-    return __float_as_uint(A) == 0x80000000u ? B : fmaf(A, h, B);
+__device__ __forceinline__ float2 run_on(float2 A, float2 h, float2 B) {
+    return __float_as_uint(A.x) == 0x80000000u ? B : fma2(A, h, B);
+}
+__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+
+// The state entering each run takes the place of its B.
+template <bool kReverse>
+__device__ __forceinline__ void enter_runs(const float* runA, float* runB, float2 h) {
+    float2 A[kWarps], B[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) A[w] = ld2(runA + w * kCh), B[w] = ld2(runB + w * kCh);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const int w = kReverse ? kWarps - 1 - i : i;
+        *reinterpret_cast<float2*>(runB + w * kCh) = h;
+        h = run_on(A[w], h, B[w]);
+    }
 }
 
-__device__ __forceinline__ unsigned long long load_word(const unsigned long long* p) {
-    unsigned long long v;
-    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
+// ---------------------------------------------------------------- the cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
-__device__ __forceinline__ uint32_t load_word(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void publish(unsigned long long* p, float A, float B) {
-    // a NaN that happens to have the pattern is made the usual one
-    uint32_t b = __float_as_uint(B);
-    if (b == ~0u) b = 0x7fffffffu;
-    const unsigned long long v = (unsigned long long)b << 32 | __float_as_uint(A);
-    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+__device__ __forceinline__ uint32_t in_block(uint32_t smem_addr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+    return a;
 }
-__device__ __forceinline__ void publish(float* p, float h) {
-    uint32_t b = __float_as_uint(h);
-    if (b == ~0u) b = 0x7fffffffu;
-    asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(b) : "memory");
-}
-
-// Before the first tile: nothing is published, the chunks' marks, states of empty sequences.
-// All blocks pass the grid's barrier before any of them looks at another's words.
-__device__ __forceinline__ void begin_chain(const ScanArgs& P, const Chain& C, const float* in, float* out) {
-    const long words = (long)C.steps * C.strips * kCh, all = (long)gridDim.x * kThreads;
-    const long me = (long)blockIdx.x * kThreads + threadIdx.x;
-    if (C.steps > 1)
-        for (long i = me; i < words; i += all) {
-            C.agg[i] = kNoAgg;
-            reinterpret_cast<uint32_t*>(C.state)[i] = kNoState;
-        }
-    if (P.cu) {
-        const int lane = threadIdx.x & 31;
-        for (long s = me / 32; s < C.steps; s += all / 32) {
-            unsigned long long first = 0, last = 0;
-            for (int half = 0; half < 2; ++half) {
-                const int t = (int)s * kTok + half * 32 + lane;
-                const int n = t < P.T ? seq_of(P, t) : 0;
-                first |= (unsigned long long)__ballot_sync(0xffffffffu, t < P.T && P.cu[n] == t) << (half * 32);
-                last |= (unsigned long long)__ballot_sync(0xffffffffu, t < P.T && P.cu[n + 1] == t + 1) << (half * 32);
-            }
-            if (lane == 0) C.marks[s] = make_ulonglong2(first, last);
-        }
-        if (out)
-            for (int n = blockIdx.x; n < P.nseq; n += gridDim.x)
-                if (P.cu[n] == P.cu[n + 1])
-                    for (long i = threadIdx.x; i < P.Z * P.d; i += kThreads)
-                        out[n * P.Z * P.d + i] = in ? in[n * P.Z * P.d + i] : 0.f;
-    }
-    if (C.steps > 1 || P.cu) cooperative_groups::this_grid().sync();
-}
-__device__ __forceinline__ ulonglong2 chunk_marks(const ScanArgs& P, const Chain& C, int chunk) {
-    if (P.cu) return __ldcg(C.marks + chunk);
-    const int left = P.T - chunk * kTok;
-    return make_ulonglong2(chunk == 0 ? 1ull : 0ull, left <= kTok ? 1ull << (left - 1) : 0ull);
-}
-
-// Thread k of the chain warps, channel k of the strip: publishes the tile's (A, B), returns the
-// state entering the tile and publishes the one leaving it.  `reset`: A is zero, the leaving state
-// does not depend on the entering one; `fresh`: the entering state is not needed.
-__device__ __forceinline__ float chain_step(const Chain& C, int step, int strip, int k, float A, float B, bool reset,
-                                            bool fresh, bool* dead, uint32_t* err) {
-    const size_t at = ((size_t)step * C.strips + strip) * kCh + k, up = (size_t)C.strips * kCh;
-    const bool more = step + 1 < C.steps;
-    if (more) {
-        if (reset) publish(C.state + at + up, B);
-        publish(C.agg + at, reset ? kCut : A, B);
-    }
-    if (fresh) return 0.f;
-    // the tiles of this grid's wave before this one publish (A, B) without waiting for states; the
-    // state before them comes from an earlier wave
-    const int J = min(min((int)blockIdx.x / C.strips, kBack), step - 1);
-    const unsigned long long* agg = C.agg + at - J * up;
-    const uint32_t* root = reinterpret_cast<const uint32_t*>(C.state) + (at - J * up);
-    unsigned long long ab[kBack];
-    uint32_t h0 = load_word(root);
-#pragma unroll
-    for (int i = 0; i < kBack; ++i) ab[i] = i < J ? load_word(agg + i * up) : 0ull;
-    uint64_t begin = 0;
-    for (;;) {
-        bool missing = h0 == kNoState;
-#pragma unroll
-        for (int i = 0; i < kBack; ++i) missing |= ab[i] == kNoAgg;
-        if (!missing || *dead) break;
-        const uint64_t now = globaltimer_ns();
-        if (begin == 0) begin = now;
-        if (now - begin > kWaitNs) {
-            atomicOr(err, kDevTimeout);
-            *dead = true;
-            break;
-        }
-        if (h0 == kNoState) h0 = load_word(root);
-#pragma unroll
-        for (int i = 0; i < kBack; ++i)
-            if (ab[i] == kNoAgg) ab[i] = load_word(agg + i * up);
-    }
-    float h = __uint_as_float(h0);
-#pragma unroll
-    for (int i = 0; i < kBack; ++i) {
-        if (i >= J) break;
-        h = run_on(__uint_as_float((uint32_t)ab[i]), h, __uint_as_float((uint32_t)(ab[i] >> 32)));
-    }
-    if (more && !reset) publish(C.state + at + up, fmaf(A, h, B));
-    return h;
+// 16 bytes into a block's shared memory, counted there by a barrier
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, float2 A, float2 B) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(__float_as_uint(A.x)), "r"(__float_as_uint(A.y)), "r"(__float_as_uint(B.x)),
+                 "r"(__float_as_uint(B.y)), "r"(bar)
+                 : "memory");
 }
 
 // One warp's arrival (its earlier shared-memory accesses are done).
@@ -267,21 +205,46 @@ __device__ __forceinline__ void wait_or_give_up(uint64_t* bar, int parity, bool*
     }
 }
 
-// 256 compute threads and 128 chain threads share the registers of 384 x 168.
-constexpr int kComputeRegs = 200, kChainRegs = 96;
-static_assert(kComputeRegs * kComputeThreads + kChainRegs * kCh <= 168 * kThreads, "more registers than the block has");
-template <int N>
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-template <typename Tin, bool kShared>
-struct FwdSmem {
-    static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
-    static constexpr int kStage = kX + kG, kStages = 3;
-    static constexpr int kRuns = kWarps * kCh;                  // floats of one value of all runs
-    static constexpr int kBytes = kStages * kStage + (4 + 2) * kRuns * 4 + 128;
-};
+// A chain thread's part of one turn: the tile's (A, B) from its runs (kReverse: last run first; no
+// tile: nothing changes), the exchange, the state entering the tile; `carry` goes from this turn's
+// first state to the next one's.  sent: [2][rank][64] x {A, B of two channels}.
+template <bool kReverse>
+__device__ __forceinline__ float2 chain_turn(const float* runA, const float* runB, bool tile, int blocks, uint32_t rank,
+                                             int n, float4* sent, uint64_t* got, float2* carry, bool* dead,
+                                             uint32_t* err) {
+    float2 A = both(1.f), B = both(0.f);
+    if (tile) {
+        bool cut = false;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const int w = kReverse ? kWarps - 1 - i : i;
+            const float2 a = ld2(runA + w * kCh);
+            cut |= __float_as_uint(a.x) == 0x80000000u;
+            B = run_on(a, B, ld2(runB + w * kCh));
+            A = mul2(A, a);
+        }
+        if (cut) A = both(kCut);
+    }
+    float2 h = *carry;
+    if (blocks == 1) {
+        *carry = run_on(A, h, B);
+        return h;
+    }
+    const int k = threadIdx.x - kComputeThreads, buf = n & 1;
+    const uint32_t to = smem_u32(sent + (buf * blocks + rank) * kChainThreads + k), bar = smem_u32(got + buf);
+    for (int q = 0; q < blocks; ++q) send(in_block(to, q), in_block(bar, q), A, B);
+    if (k == 0) mbar_arrive_expect_tx(got + buf, blocks * kChainThreads * 16);
+    wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
+    float2 mine = h;
+    const float4* all = sent + buf * blocks * kChainThreads + k;
+    for (int q = 0; q < blocks; ++q) {
+        const float4 v = all[q * kChainThreads];
+        if (q == (int)rank) mine = h;
+        h = run_on(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
+    }
+    *carry = h;
+    return mine;
+}
 
 // The gates of one token: of a channel each, or one for all.
 template <bool kShared>
@@ -312,31 +275,48 @@ __device__ __forceinline__ void token_gates(int rule, const float* gt, float gs,
 }
 
 template <typename Tin, bool kShared>
-__global__ void __launch_bounds__(kThreads, 1) scan_fwd_kernel(ScanArgs P, Chain C, int tiles) {
+struct FwdSmem {
+    static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
+    static constexpr int kStage = kX + kG, kStages = 2;
+    static constexpr int kRuns = kWarps * kCh;                  // floats of one value of all runs
+    static constexpr int bytes(int blocks) { return kStages * kStage + 2 * kRuns * 4 + 2 * blocks * kChainThreads * 16 + 256; }
+};
+
+template <typename Tin, bool kShared>
+__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, int blocks, int steps) {
     using M = FwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
-    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [2][A, B][warp][128]
-    float* entering = runs + 4 * M::kRuns;                                     // [2][warp][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(entering + 2 * M::kRuns);
-    uint64_t* ready = full + M::kStages;      // a tile's (A, B) of all runs are there
-    uint64_t* entered = ready + 2;            // the states entering them are
+    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [A, B (then: entering)][warp][128]
+    float4* sent = reinterpret_cast<float4*>(runs + 2 * M::kRuns);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sent + 2 * blocks * kChainThreads);
+    uint64_t* ready = full + M::kStages;      // the tile's (A, B) of all runs are there
+    uint64_t* entered = ready + 1;            // the states entering them are
+    uint64_t* got = entered + 1;              // [2] all blocks' (A, B) are
+    uint2* marks = reinterpret_cast<uint2*>(got + 2);
     const Strips S(P.Z, P.d);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
+    const int strip = blockIdx.x / blocks, turns = (steps + blocks - 1) / blocks;
     const Tin* x = static_cast<const Tin*>(P.x);
     Tin* o = static_cast<Tin*>(P.o);
     if (threadIdx.x == 0) {
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(ready + i, kWarps), mbar_init(entered + i, kCh / 32);
+        mbar_init(ready, kWarps);
+        mbar_init(entered, kChainThreads / 32);
+        mbar_init(got, 1);
+        mbar_init(got + 1, 1);
         fence_mbar_init();
     }
     __syncthreads();
-    const int count = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     auto prefetch = [&](int n) {      // by the last warp
-        if (n >= count) return;
-        const int tile = blockIdx.x + n * gridDim.x, st = n % M::kStages;
-        const int strip = tile % S.count, t0 = tile / S.count * kTok, rows = min(kTok, P.T - t0);
-        if (lane == 0)
+        const int chunk = n * blocks + rank;
+        if (chunk >= steps) return;
+        const int st = n % M::kStages, t0 = chunk * kTok, rows = min(kTok, P.T - t0);
+        const uint2 m = chunk_marks(P, chunk);
+        if (lane == 0) {
+            marks[n % kMarks] = m;
             mbar_arrive_expect_tx(full + st, rows * strip_channels(S, P.Z, P.d, strip) * (int)(sizeof(Tin) + (kShared ? 0 : 4)));
+        }
         __syncwarp();
         char* dst = smem + st * M::kStage;
         stage(reinterpret_cast<Tin*>(dst), x, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
@@ -344,155 +324,158 @@ __global__ void __launch_bounds__(kThreads, 1) scan_fwd_kernel(ScanArgs P, Chain
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
-    begin_chain(P, C, P.S0, P.S_T);
+    pass_empty(P, P.S0, P.S_T);
+    if (blocks > 1) cluster_sync();       // every block's barriers are set up
     bool dead = false;
 
-    if (warp >= kWarps) {             // the chain
-        fewer_registers<kChainRegs>();
-        const int k = threadIdx.x - kComputeThreads;
-        for (int n = 0; n < count; ++n) {
-            const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
-            const ulonglong2 m = chunk_marks(P, C, step);
-            wait_or_give_up(ready + (n & 1), n >> 1 & 1, &dead, P.err);
-            if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);
-            const float* ra = runs + (n & 1) * 2 * M::kRuns + k;
-            float A[kWarps], B[kWarps], tA = 1.f, tB = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                A[w] = ra[w * kCh];
-                B[w] = ra[M::kRuns + w * kCh];
-                tB = run_on(A[w], tB, B[w]);
-                tA *= A[w];
+    if (warp >= kWarps) {                 // the chain
+        const int k = (threadIdx.x - kComputeThreads) * 2;
+        float2 carry = both(0.f);
+        for (int n = 0; n < turns; ++n) {
+            const int chunk = n * blocks + rank;
+            const bool tile = chunk < steps;
+            if (tile) {
+                wait_or_give_up(ready, n & 1, &dead, P.err);
+                if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);      // the stage has been read
             }
-            float h = chain_step(C, step, strip, k, tA, tB, m.x != 0, m.x & 1ull, &dead, P.err);
-            float* en = entering + (n & 1) * M::kRuns + k;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                en[w * kCh] = h;
-                h = run_on(A[w], h, B[w]);
+            const float2 h = chain_turn<false>(runs + k, runs + M::kRuns + k, tile, blocks, rank, n, sent, got, &carry,
+                                               &dead, P.err);
+            if (tile) {
+                enter_runs<false>(runs + k, runs + M::kRuns + k, h);
+                warp_arrive(entered);
+                if (P.E) *reinterpret_cast<float2*>(P.E + ((size_t)chunk * S.count + strip) * kCh + k) = h;
             }
-            warp_arrive(entered + (n & 1));
         }
-        return;
-    }
-    more_registers<kComputeRegs>();
-
-    struct Set {
-        Gate<kShared> a;
-        P4 b[kRun];
-    };
-    auto reduce = [&](Set& s, int n) {
-        const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
-        const int tw = step * kTok + warp * kRun, st = n % M::kStages;
-        const Lane L = lane_of(S, P.Z, P.d, strip, lane);
-        const uint32_t first = (uint32_t)(chunk_marks(P, C, step).x >> (warp * kRun)) & ((1u << kRun) - 1u);
-        const bool plain = first == 0 && tw + kRun <= P.T;
-        float gs[kRun];
-        if (kShared) {
+    } else {
+        const Lane lanes(S, P.Z, P.d, lane);
+        const Spot L = spot_of(lanes, strip);
+        const int mine = lanes.smem + warp * kRun * lanes.row;
+        float* run = runs + warp * kCh + lane * 4;
+        for (int n = 0; n < turns; ++n) {
+            const int chunk = n * blocks + rank;
+            if (chunk >= steps) break;
+            const int tw = chunk * kTok + warp * kRun, st = n % M::kStages;
+            float gs[kRun];
+            if (kShared) {
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
-        }
-        wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
-        const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + L.smem + warp * kRun * L.row;
-        const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + M::kX) + L.smem + warp * kRun * L.row;
-        P4 ra = all4(1.f), rb = all4(0.f);
+                for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
+            }
+            wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
+            const uint2 m = marks[n % kMarks];
+            const uint32_t first = run_bits(m.x, warp);
+            const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + mine;
+            const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + M::kX) + mine;
+            // 1. the run's tokens as h = a h' + b, and the run's (A, B)
+            Gate<kShared> a;
+            P4 b[kRun];
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            P4 a, w, dw;
-            token_gates<kShared, false>(P.rule, gt + i * L.row, gs[i], &a, &w, &dw);
-            P4 b = mul4(w, ld4(xs + i * L.row));
-            if (!plain) {
-                if (tw + i >= P.T) {             // behind the end: a token that changes nothing
-                    a = all4(1.f);
-                    b = all4(0.f);
+            for (int i = 0; i < kRun; ++i) {
+                P4 a1, w, dw;
+                token_gates<kShared, false>(P.rule, gt + i * lanes.row, gs[i], &a1, &w, &dw);
+                a.set(i, a1);
+                b[i] = mul4(w, ld4(xs + i * lanes.row));
+            }
+            if (tw + kRun > P.T) {            // behind the end: tokens that change nothing
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (tw + i >= P.T) {
+                        a.set(i, all4(1.f));
+                        b[i] = all4(0.f);
+                    }
+            }
+            for (uint32_t bits = first; bits; bits &= bits - 1) {     // a sequence begins: its own state enters
+                const int from = __ffs(bits) - 1;
+                const P4 s0 = P.S0 && L.on ? ld4(P.S0 + ((long)seq_of(P, tw + from) * P.Z + L.z) * P.d + L.c) : all4(0.f);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (i == from) {
+                        b[i] = fma4(a.at(i), s0, b[i]);
+                        a.set(i, all4(0.f));
+                    }
+            }
+            P4 ra = all4(1.f), rb = all4(0.f);
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                if (first >> i & 1u) rb = all4(0.f);
+                ra = mul4(ra, a.at(i));
+                rb = fma4(a.at(i), rb, b[i]);
+            }
+            if (first) ra = all4(kCut);
+            st4(run, ra);
+            st4(run + M::kRuns, rb);
+            warp_arrive(ready);
+            // 3. the outputs
+            wait_or_give_up(entered, n & 1, &dead, P.err);
+            P4 h = ld4(run + M::kRuns);
+            const uint32_t last = P.S_T ? run_bits(m.y, warp) : 0u;
+            const int live = L.on ? P.T - tw : 0;
+            if (!o && !last) continue;
+            Tin* out = o + (L.z * P.T + tw) * P.d + L.c;
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                if (first >> i & 1u) h = all4(0.f);          // its state is in b
+                h = fma4(a.at(i), h, b[i]);
+                if (o && i < live) st4(out + i * P.d, h);
+                if (last >> i & 1u) {                        // a sequence ends
+                    if (L.on) st4(P.S_T + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, h);
                 }
-                if (first >> i & 1u) {           // a sequence begins: its own state enters, no other
-                    const int q = seq_of(P, tw + i);
-                    if (P.S0 && L.on) b = fma4(a, ld4(P.S0 + ((long)q * P.Z + L.z) * P.d + L.c), b);
-                    a = rb = all4(0.f);
-                }
             }
-            ra = mul4(ra, a);
-            rb = fma4(a, rb, b);
-            s.a.set(i, a);
-            s.b[i] = b;
         }
-        float* out = runs + (n & 1) * 2 * M::kRuns + warp * kCh + lane * 4;
-        if (first) ra = all4(kCut);
-        st4(out, ra);
-        st4(out + M::kRuns, rb);
-        warp_arrive(ready + (n & 1));
-    };
-    auto finish = [&](const Set& s, int n) {
-        const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
-        const int tw = step * kTok + warp * kRun;
-        const Lane L = lane_of(S, P.Z, P.d, strip, lane);
-        const ulonglong2 m = chunk_marks(P, C, step);
-        const uint32_t first = (uint32_t)(m.x >> (warp * kRun)) & ((1u << kRun) - 1u);
-        const uint32_t last = (uint32_t)(m.y >> (warp * kRun)) & ((1u << kRun) - 1u);
-        wait_or_give_up(entered + (n & 1), n >> 1 & 1, &dead, P.err);
-        P4 h = ld4(entering + (n & 1) * M::kRuns + warp * kCh + lane * 4);
-        Tin* out = o ? o + (L.z * P.T + tw) * P.d + L.c : nullptr;
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            if (first >> i & 1u) h = all4(0.f);          // its state is in b
-            h = fma4(s.a.at(i), h, s.b[i]);
-            if (o && L.on && tw + i < P.T) st4(out + i * P.d, h);
-            if (P.S_T && (last >> i & 1u) && L.on) st4(P.S_T + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, h);
-        }
-    };
-    Set s0, s1;      // a tile's run waits in one set while the next one is reduced into the other
-    for (int n = 0; n < count; n += 2) {
-        reduce(s0, n);
-        if (n > 0) finish(s1, n - 1);
-        if (n + 1 < count) reduce(s1, n + 1);
-        finish(s0, n);
     }
-    if (count % 2 == 0) finish(s1, count - 1);
+    if (blocks > 1) cluster_sync();       // no block leaves while another may still send to it
 }
 
 // The reverse pass.  c = e^{g_t} G_t flows from token t into t - 1 (dS_T into a sequence's last
 // token), G_t = dO_t + c: affine again, c_out = A c_in + R over a run, and the tiles are taken
 // from the last to the first.  A tile's own states are put together again from the state that
-// the forward kept for it, so no state but one of 64 tokens is ever stored.
+// the forward kept for it, so no state but one of 32 tokens is ever stored.
 template <typename Tin, bool kShared>
 struct BwdSmem {
     static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
     static constexpr int kStage = 2 * kX + kG, kStages = 2;
     static constexpr int kRuns = kWarps * kCh;
-    static constexpr int kBytes = kStages * kStage + 6 * kRuns * 4 + 128;
+    static constexpr int bytes(int blocks) { return kStages * kStage + 4 * kRuns * 4 + 2 * blocks * kChainThreads * 16 + 256; }
 };
 
 template <typename Tin, bool kShared>
-__global__ void __launch_bounds__(kThreads, 1) scan_bwd_kernel(ScanArgs P, Chain C, const float* states, float* parts,
-                                                               int tiles) {
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const float* states, float* parts, int blocks,
+                                                               int steps) {
     using M = BwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
-    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [A, B, reverse A, R][warp][128]
-    float* entering = runs + 4 * M::kRuns;                                     // [state, flow][warp][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(entering + 2 * M::kRuns);
+    // [A, B (then: the state entering), reverse A, R (then: the flow entering)][warp][128]
+    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);
+    float4* sent = reinterpret_cast<float4*>(runs + 4 * M::kRuns);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sent + 2 * blocks * kChainThreads);
     uint64_t* spent = full + M::kStages;      // a stage has been read to its end
     uint64_t* ready = spent + M::kStages;
     uint64_t* entered = ready + 1;
+    uint64_t* got = entered + 1;
+    uint2* marks = reinterpret_cast<uint2*>(got + 2);
     const Strips S(P.Z, P.d);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
+    const int strip = blockIdx.x / blocks, turns = (steps + blocks - 1) / blocks;
     const Tin* x = static_cast<const Tin*>(P.x);
     const Tin* dO = static_cast<const Tin*>(P.dO);
     if (threadIdx.x == 0) {
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1), mbar_init(spent + i, kWarps);
         mbar_init(ready, kWarps);
-        mbar_init(entered, kCh / 32);
+        mbar_init(entered, kChainThreads / 32);
+        mbar_init(got, 1);
+        mbar_init(got + 1, 1);
         fence_mbar_init();
     }
     __syncthreads();
-    const int count = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     auto prefetch = [&](int n) {
-        if (n >= count) return;
-        const int tile = blockIdx.x + n * gridDim.x, st = n % M::kStages;
-        const int strip = tile % S.count, t0 = (C.steps - 1 - tile / S.count) * kTok, rows = min(kTok, P.T - t0);
-        if (lane == 0)
+        const int chunk = steps - 1 - (n * blocks + (int)rank);
+        if (chunk < 0) return;
+        const int st = n % M::kStages, t0 = chunk * kTok, rows = min(kTok, P.T - t0);
+        const uint2 m = chunk_marks(P, chunk);
+        if (lane == 0) {
+            marks[n % kMarks] = m;
             mbar_arrive_expect_tx(full + st,
                                   rows * strip_channels(S, P.Z, P.d, strip) * (int)(2 * sizeof(Tin) + (kShared ? 0 : 4)));
+        }
         __syncwarp();
         char* dst = smem + st * M::kStage;
         stage(reinterpret_cast<Tin*>(dst), x, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
@@ -501,158 +484,168 @@ __global__ void __launch_bounds__(kThreads, 1) scan_bwd_kernel(ScanArgs P, Chain
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
-    begin_chain(P, C, P.dST, P.dS0);
+    pass_empty(P, P.dST, P.dS0);
+    if (blocks > 1) cluster_sync();
     bool dead = false;
 
     if (warp >= kWarps) {             // the chain
-        fewer_registers<kChainRegs>();
-        const int k = threadIdx.x - kComputeThreads;
-        for (int n = 0; n < count; ++n) {
-            const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
-            const int chunk = C.steps - 1 - step;
-            const ulonglong2 m = chunk_marks(P, C, chunk);
-            float h = m.x & 1ull ? 0.f : states[((size_t)chunk * S.count + strip) * kCh + k];
-            wait_or_give_up(ready, n & 1, &dead, P.err);
-            float A[kWarps], B[kWarps], tA = 1.f, tB = 0.f;
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                A[w] = runs[2 * M::kRuns + w * kCh + k];
-                B[w] = runs[3 * M::kRuns + w * kCh + k];
-                tB = run_on(A[w], tB, B[w]);
-                tA *= A[w];
+        const int k = (threadIdx.x - kComputeThreads) * 2;
+        float2 carry = both(0.f);
+        for (int n = 0; n < turns; ++n) {
+            const int chunk = steps - 1 - (n * blocks + (int)rank);
+            const bool tile = chunk >= 0;
+            float2 h = both(0.f);
+            if (tile) {
+                if (chunk > 0) h = ld2(states + ((size_t)chunk * S.count + strip) * kCh + k);
+                wait_or_give_up(ready, n & 1, &dead, P.err);
             }
-            const bool at_end = P.T - chunk * kTok <= kTok || (m.y >> (kTok - 1) & 1ull);     // nothing flows in
-            float c = chain_step(C, step, strip, k, tA, tB, m.y != 0, at_end, &dead, P.err);
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                entering[M::kRuns + w * kCh + k] = c;
-                c = run_on(A[w], c, B[w]);
-            }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                entering[w * kCh + k] = h;
-                h = run_on(runs[w * kCh + k], h, runs[M::kRuns + w * kCh + k]);
-            }
-            warp_arrive(entered);
-            if (warp == kThreads / 32 - 1 && n + M::kStages < count) {
-                wait_or_give_up(spent + n % M::kStages, n / M::kStages & 1, &dead, P.err);
-                prefetch(n + M::kStages);
+            const float2 c = chain_turn<true>(runs + 2 * M::kRuns + k, runs + 3 * M::kRuns + k, tile, blocks, rank, n, sent,
+                                              got, &carry, &dead, P.err);
+            if (tile) {
+                enter_runs<true>(runs + 2 * M::kRuns + k, runs + 3 * M::kRuns + k, c);
+                enter_runs<false>(runs + k, runs + M::kRuns + k, h);
+                warp_arrive(entered);
+                if (warp == kThreads / 32 - 1 && chunk - M::kStages * blocks >= 0) {
+                    wait_or_give_up(spent + n % M::kStages, n / M::kStages & 1, &dead, P.err);
+                    prefetch(n + M::kStages);
+                }
             }
         }
-        return;
+    } else {
+        const Lane lanes(S, P.Z, P.d, lane);
+        const Spot L = spot_of(lanes, strip);
+        const int mine = lanes.smem + warp * kRun * lanes.row;
+        for (int n = 0; n < turns; ++n) {
+            const int chunk = steps - 1 - (n * blocks + (int)rank);
+            if (chunk < 0) break;
+            const int tw = chunk * kTok + warp * kRun, st = n % M::kStages;
+            const bool ragged = tw + kRun > P.T;
+            float gs[kRun];
+            if (kShared) {
+    #pragma unroll
+                for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
+            }
+            wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
+            const uint2 m = marks[n % kMarks];
+            const uint32_t first = run_bits(m.x, warp), last = run_bits(m.y, warp);
+            const int off = mine;
+            const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + off;
+            const Tin* us = reinterpret_cast<const Tin*>(smem + st * M::kStage + M::kX) + off;
+            const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + 2 * M::kX) + off;
+            auto row_of = [&](int i) { return ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c; };
+            auto row = [&](const float* from, int i) { return from && L.on ? ld4(from + row_of(i)) : all4(0.f); };
+            // 1. the gates, and the run's (A, B) forward and in reverse
+            Gate<kShared> a, w, dw;
+    #pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                P4 a1, w1, dw1;
+                token_gates<kShared, true>(P.rule, gt + i * lanes.row, gs[i], &a1, &w1, &dw1);
+                if (ragged && tw + i >= P.T) a1 = all4(1.f), w1 = dw1 = all4(0.f);
+                a.set(i, a1);
+                w.set(i, w1);
+                dw.set(i, dw1);
+            }
+            // (tokens behind the end are staged as whatever the stage held)
+            auto x_at = [&](int i) { return ragged && tw + i >= P.T ? all4(0.f) : ld4(xs + i * lanes.row); };
+            auto u_at = [&](int i) { return ragged && tw + i >= P.T ? all4(0.f) : ld4(us + i * lanes.row); };
+            const int cut = 31 - __clz(first);         // the last begin in the run; -1: none
+            P4 ra = all4(1.f), rb = all4(0.f), edge = all4(0.f);
+            if (first) edge = row(P.S0, cut);
+    #pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                if (i == cut) rb = edge;
+                ra = mul4(ra, a.at(i));
+                rb = fma4(a.at(i), rb, mul4(w.at(i), x_at(i)));
+            }
+            if (first) ra = all4(kCut);
+            float* out = runs + warp * kCh + lane * 4;
+            st4(out, ra);
+            st4(out + M::kRuns, rb);
+            ra = all4(1.f);
+            rb = all4(0.f);
+            const int stop = __ffs(last) - 1;          // the first end in the run
+            if (last) edge = row(P.dST, stop);
+    #pragma unroll
+            for (int i = kRun - 1; i >= 0; --i) {
+                if (i == stop) rb = edge;
+                ra = mul4(ra, a.at(i));
+                rb = mul4(a.at(i), add4(u_at(i), rb));
+            }
+            if (last) ra = all4(kCut);
+            st4(out + 2 * M::kRuns, ra);
+            st4(out + 3 * M::kRuns, rb);
+            warp_arrive(ready);
+            wait_or_give_up(entered, n & 1, &dead, P.err);
+            // 2. the states before the run's tokens: e = a h' + w' x
+            P4 e[kRun], G[kRun];
+            P4 h = ld4(out + M::kRuns);
+    #pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const P4 xv = x_at(i);
+                e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
+                h = fma4(a.at(i), h, mul4(w.at(i), xv));
+            }
+            for (uint32_t bits = first; bits; bits &= bits - 1) {       // once more from where a sequence begins
+                const int from = __ffs(bits) - 1;
+                h = row(P.S0, from);
+    #pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (i >= from) {
+                        const P4 xv = x_at(i);
+                        e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
+                        h = fma4(a.at(i), h, mul4(w.at(i), xv));
+                    }
+            }
+            // 3. the gradients
+            P4 c = ld4(out + 3 * M::kRuns);
+    #pragma unroll
+            for (int i = kRun - 1; i >= 0; --i) {
+                G[i] = add4(u_at(i), c);
+                c = mul4(a.at(i), G[i]);
+            }
+            for (uint32_t bits = last; bits;) {                         // once more from where a sequence ends
+                const int from = 31 - __clz(bits);
+                bits ^= 1u << from;
+                c = row(P.dST, from);
+    #pragma unroll
+                for (int i = kRun - 1; i >= 0; --i)
+                    if (i <= from) {
+                        G[i] = add4(u_at(i), c);
+                        c = mul4(a.at(i), G[i]);
+                    }
+            }
+            const int live = L.on ? P.T - tw : 0;
+            float* dx = P.dx + (L.z * P.T + tw) * P.d + L.c;
+            float* dg = P.dg + (L.z * P.T + tw) * (kShared ? 1 : P.d) + (kShared ? 0 : L.c);
+    #pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const P4 dgv = mul4(e[i], G[i]);
+                if (i < live) {
+                    st4(dx + i * P.d, mul4(w.at(i), G[i]));
+                    if (!kShared) st4(dg + i * P.d, dgv);
+                }
+                if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
+                    float sum = i < live ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
+                    for (int far = S.heads > 1 ? S.dv / 2 : 16; far > 0; far >>= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, far);
+                    if (i < live && (S.heads > 1 ? lane % S.dv == 0 : lane == 0)) {
+                        if (S.per_head == 1) dg[i] = sum;
+                        else parts[((long)(strip % S.per_head) * P.Z + L.z) * P.T + tw + i] = sum;
+                    }
+                }
+            }
+            for (uint32_t bits = P.dS0 ? first : 0u; bits; bits &= bits - 1) {
+                const int from = __ffs(bits) - 1;
+                P4 d0 = all4(0.f);
+    #pragma unroll
+                for (int i = 0; i < kRun; ++i)
+                    if (i == from) d0 = mul4(a.at(i), G[i]);
+                if (L.on) st4(P.dS0 + row_of(from), d0);
+            }
+            warp_arrive(spent + st);
+        }
     }
-    more_registers<kComputeRegs>();
-
-    for (int n = 0; n < count; ++n) {
-        const int tile = blockIdx.x + n * gridDim.x, strip = tile % S.count, step = tile / S.count;
-        const int chunk = C.steps - 1 - step, tw = chunk * kTok + warp * kRun, st = n % M::kStages;
-        const Lane L = lane_of(S, P.Z, P.d, strip, lane);
-        const ulonglong2 m = chunk_marks(P, C, chunk);
-        const uint32_t first = (uint32_t)(m.x >> (warp * kRun)) & ((1u << kRun) - 1u);
-        const uint32_t last = (uint32_t)(m.y >> (warp * kRun)) & ((1u << kRun) - 1u);
-        const bool plain = (first | last) == 0 && tw + kRun <= P.T;
-        float gs[kRun];
-        if (kShared) {
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
-        }
-        wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
-        const int off = L.smem + warp * kRun * L.row;
-        const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + off;
-        const Tin* us = reinterpret_cast<const Tin*>(smem + st * M::kStage + M::kX) + off;
-        const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + 2 * M::kX) + off;
-        auto state0 = [&](const float* from, int t) {      // a sequence's row of S0 or dS_T
-            return from && L.on ? ld4(from + ((long)seq_of(P, t) * P.Z + L.z) * P.d + L.c) : all4(0.f);
-        };
-        // 1. the gates, and the run's (A, B) forward and in reverse
-        Gate<kShared> a, w, dw;
-        P4 ra = all4(1.f), rb = all4(0.f);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            P4 a1, w1, dw1;
-            token_gates<kShared, true>(P.rule, gt + i * L.row, gs[i], &a1, &w1, &dw1);
-            if (!plain) {
-                if (tw + i >= P.T) {
-                    a1 = all4(1.f);
-                    w1 = dw1 = all4(0.f);
-                }
-                if (first >> i & 1u) {
-                    ra = all4(0.f);
-                    rb = state0(P.S0, tw + i);
-                }
-            }
-            ra = mul4(ra, a1);
-            P4 b = mul4(w1, ld4(xs + i * L.row));
-            if (!plain && tw + i >= P.T) b = all4(0.f);     // the stage holds anything there
-            rb = fma4(a1, rb, b);
-            a.set(i, a1);
-            w.set(i, w1);
-            dw.set(i, dw1);
-        }
-        float* out = runs + warp * kCh + lane * 4;
-        if (first) ra = all4(kCut);
-        st4(out, ra);
-        st4(out + M::kRuns, rb);
-        ra = all4(1.f);
-        rb = all4(0.f);
-#pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
-            P4 u = ld4(us + i * L.row);
-            if (!plain) {
-                if (tw + i >= P.T) u = all4(0.f);
-                if (last >> i & 1u) {
-                    ra = all4(0.f);
-                    rb = state0(P.dST, tw + i);
-                }
-            }
-            ra = mul4(ra, a.at(i));
-            rb = mul4(a.at(i), add4(u, rb));
-        }
-        if (last) ra = all4(kCut);
-        st4(out + 2 * M::kRuns, ra);
-        st4(out + 3 * M::kRuns, rb);
-        warp_arrive(ready);
-        wait_or_give_up(entered, n & 1, &dead, P.err);
-        // 2. the states before the run's tokens: e = a h' + w' x
-        P4 e[kRun];
-        P4 h = ld4(entering + warp * kCh + lane * 4);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            if (!plain && (first >> i & 1u)) h = state0(P.S0, tw + i);
-            const P4 xv = ld4(xs + i * L.row);
-            e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
-            h = fma4(a.at(i), h, mul4(w.at(i), xv));
-        }
-        // 3. the gradients
-        P4 c = ld4(entering + M::kRuns + warp * kCh + lane * 4);
-        float* dx = P.dx + (L.z * P.T + tw) * P.d + L.c;
-        float* dg = P.dg + (L.z * P.T + tw) * (kShared ? 1 : P.d) + (kShared ? 0 : L.c);
-#pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
-            const bool live = L.on && tw + i < P.T;
-            if (!plain && (last >> i & 1u)) c = state0(P.dST, tw + i);
-            const P4 G = add4(ld4(us + i * L.row), c);
-            const P4 dgv = mul4(e[i], G);
-            c = mul4(a.at(i), G);
-            if (!plain && tw + i >= P.T) c = all4(0.f);      // behind the end; the last token's own comes next
-            if (live) {
-                st4(dx + i * P.d, mul4(w.at(i), G));
-                if (!kShared) st4(dg + i * P.d, dgv);
-            }
-            if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
-                float sum = live ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
-                for (int far = S.heads > 1 ? S.dv / 2 : 16; far > 0; far >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, far);
-                if (live && (S.heads > 1 ? lane % S.dv == 0 : lane == 0)) {
-                    if (S.per_head == 1) dg[i] = sum;
-                    else parts[((long)(strip % S.per_head) * P.Z + L.z) * P.T + tw + i] = sum;
-                }
-            }
-            if (!plain && P.dS0 && (first >> i & 1u) && L.on)
-                st4(P.dS0 + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, c);
-        }
-        warp_arrive(spent + st);
-    }
+    if (blocks > 1) cluster_sync();
 }
 
 __global__ void __launch_bounds__(256) scan_parts_kernel(const float* __restrict__ parts, float* __restrict__ dg,
@@ -695,86 +688,111 @@ static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 static long scan_steps(int T) { return ((long)T + kTok - 1) / kTok; }
 
 size_t scan_states_bytes(long Z, int T, int d) { return (size_t)scan_steps(T) * Strips(Z, d).count * kCh * sizeof(float); }
-// (A, B) of every tile and the chunks' marks; backward: also the flows between tiles, and the
-// partial sums of a shared decay's gradient where a head is wider than a strip
+// the partial sums of a shared decay's gradient where a head is wider than a strip
 size_t scan_scratch_bytes(long Z, int T, int d, int gw, bool backward) {
     const Strips S(Z, d);
-    const size_t tiles = (size_t)scan_steps(T) * S.count;
-    size_t n = tiles * kCh * sizeof(unsigned long long) + up256(scan_steps(T) * sizeof(ulonglong2));
-    if (backward) {
-        n += tiles * kCh * sizeof(float);
-        if (gw == 1 && S.per_head > 1) n += up256((size_t)S.per_head * Z * T * sizeof(float));
-    }
-    return n;
+    return backward && gw == 1 && S.per_head > 1 ? up256((size_t)S.per_head * Z * T * sizeof(float)) : 0;
 }
 
 namespace {
 
-// Launches with every block resident at once, at most one per tile.
+// How many clusters of each size a device holds at once, asked once per device and kernel.
+struct Room {
+    std::atomic<int> clusters[5];      // of 1, 2, 4, 8, 16 blocks
+    std::atomic<int> sms;
+};
+
+template <typename Kernel>
+cudaError_t config(Kernel kernel, int blocks, int smem, long strips, cudaStream_t stream, cudaLaunchConfig_t* cfg,
+                   cudaLaunchAttribute* attr) {
+    *cfg = cudaLaunchConfig_t{};
+    cfg->gridDim = dim3((unsigned)(strips * blocks));
+    cfg->blockDim = dim3(kThreads);
+    cfg->dynamicSmemBytes = (size_t)smem;
+    cfg->stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = blocks > 1 ? 1 : 0;
+    return cudaSuccess;
+}
+
+template <typename Kernel>
+cudaError_t find_room(Kernel kernel, int (*smem)(int), Room* room) {
+    int dev = 0, sms = 0;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(kCluster))) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+    for (int i = 0; i < 5; ++i) {
+        int n = 0;
+        if (i == 0) {
+            if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem(1))) != cudaSuccess) return e;
+            n *= sms;
+        } else {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute attr[1];
+            config(kernel, 1 << i, smem(1 << i), 64, nullptr, &cfg, attr);
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();       // a size that this device does not run
+                n = 0;
+            }
+        }
+        room->clusters[i].store(n, std::memory_order_relaxed);
+    }
+    room->sms.store(sms, std::memory_order_release);
+    return cudaSuccess;
+}
+
+// Blocks per cluster: with rounds = strips / clusters held at once, a strip's turns are
+// ceil(steps / blocks), and a turn takes as long as the blocks that share an SM, or, for fewer
+// than two, as its own latency (about 1.6 of a block's share at full rate).
+int pick_blocks(const Room& room, long strips, long steps) {
+    int best = 1;
+    double least = 0;
+    for (int i = 0; i < 5; ++i) {
+        const int n = room.clusters[i].load(std::memory_order_relaxed), blocks = 1 << i;
+        if (n == 0 || (i > 0 && steps <= blocks / 2)) continue;
+        const long held = strips < n ? strips : n, sms = room.sms.load(std::memory_order_relaxed);
+        const double share = (double)((held * blocks + sms - 1) / sms);
+        const double cost = (double)((strips + n - 1) / n) * (double)((steps + blocks - 1) / blocks) * (share < 1.6 ? 1.6 : share);
+        if (i == 0 || cost < least) best = blocks, least = cost;
+    }
+    return best;
+}
+
 template <typename Kernel, typename... Args>
-cudaError_t launch_tiles(Kernel kernel, int smem, std::atomic<int>* resident, bool waits, long tiles,
-                         cudaStream_t stream, Args... args) {
+cudaError_t launch_clusters(Kernel kernel, int (*smem)(int), Room* rooms, const ScanArgs& a, cudaStream_t stream,
+                            Args... args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int most = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
-    if (most == 0) {
-        int sms = 0, per = 0;
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-        // the register split of compute and chain warps fits what the block is launched with
-        cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-        if (fa.numRegs * kThreads < kComputeRegs * kComputeThreads + kChainRegs * kCh) return cudaErrorInvalidConfiguration;
-        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem)) != cudaSuccess) return e;
-        most = sms * per;
-        if (dev < 64) resident[dev].store(most, std::memory_order_relaxed);
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < most ? tiles : most));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    Room& room = rooms[dev];
+    if (room.sms.load(std::memory_order_acquire) == 0 && (e = find_room(kernel, smem, &room)) != cudaSuccess) return e;
+    const long strips = Strips(a.Z, a.d).count, steps = scan_steps(a.T);
+    const int blocks = pick_blocks(room, strips, steps);
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = waits ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-Chain scan_chain(const ScanArgs& a, float* states, long* tiles) {
-    Chain C;
-    C.strips = Strips(a.Z, a.d).count;
-    C.steps = (int)scan_steps(a.T);
-    *tiles = (long)C.steps * C.strips;
-    C.agg = static_cast<unsigned long long*>(a.scratch);
-    C.marks = reinterpret_cast<ulonglong2*>(C.agg + (size_t)*tiles * kCh);
-    C.state = states ? states
-                     : reinterpret_cast<float*>(reinterpret_cast<char*>(C.marks) + up256(C.steps * sizeof(ulonglong2)));
-    return C;
+    config(kernel, blocks, smem(blocks), strips, stream, &cfg, attr);
+    return cudaLaunchKernelEx(&cfg, kernel, a, args..., blocks, (int)steps);
 }
 
 template <typename Tin, bool kShared>
 cudaError_t launch_fwd(const ScanArgs& a, cudaStream_t stream) {
-    static std::atomic<int> resident[64];
-    long tiles;
-    const Chain C = scan_chain(a, a.E, &tiles);
-    if (tiles >= (1l << 31)) return cudaErrorInvalidValue;
-    return launch_tiles(scan_fwd_kernel<Tin, kShared>, FwdSmem<Tin, kShared>::kBytes, resident, C.steps > 1 || a.cu, tiles,
-                        stream, a, C, (int)tiles);
+    static Room rooms[64];
+    return launch_clusters(scan_fwd_kernel<Tin, kShared>, FwdSmem<Tin, kShared>::bytes, rooms, a, stream);
 }
 
 template <typename Tin, bool kShared>
 cudaError_t launch_bwd(const ScanArgs& a, cudaStream_t stream) {
-    static std::atomic<int> resident[64];
-    long tiles;
-    const Chain C = scan_chain(a, nullptr, &tiles);
-    if (tiles >= (1l << 31)) return cudaErrorInvalidValue;
+    static Room rooms[64];
     const int per_head = Strips(a.Z, a.d).per_head;
-    float* parts = C.state + (size_t)tiles * kCh;
-    cudaError_t e = launch_tiles(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::kBytes, resident,
-                                 C.steps > 1 || a.cu, tiles, stream, a, C, (const float*)a.E, parts, (int)tiles);
+    float* parts = static_cast<float*>(a.scratch);
+    const cudaError_t e = launch_clusters(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::bytes, rooms, a, stream,
+                                          (const float*)a.E, parts);
     if (e != cudaSuccess || !kShared || per_head == 1) return e;
     const long n = a.Z * a.T, blocks = (n + 255) / 256;
     scan_parts_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(parts, a.dg, n, per_head);
