@@ -1,20 +1,25 @@
 // efla_scan.cu -- the per-channel gated linear recurrence: forward, backward, one token.
 //
 // The recurrence is affine in the state: over any run of tokens h_out = A h_in + B, and runs
-// compose.  A tile is 32 tokens x 128 channels (a "strip").  A cluster of blocks takes one strip
-// along time: in each turn its blocks hold consecutive tiles, and
-//   1. the eight compute warps reduce four tokens each (a lane holds four channels) to (A, B);
-//   2. the two chain warps (a thread holds two channels) fold these to the tile's (A, B), write it
-//      into the shared memory of every block of the cluster, and fold what all blocks sent onto
-//      the state the turn began with: the state entering the block's own tile, the one entering
-//      each of its runs, and the one that the next turn begins with, which is thus known to every
-//      block without another exchange;
+// compose.  A strip is 128, 64 or 32 channels, a tile 32, 64 or 128 tokens of it (4096 values).
+// A cluster of blocks takes one strip along time: in each turn its blocks hold consecutive tiles,
+// and
+//   1. the eight compute warps reduce runs of four tokens (a lane: four channels of one run) to
+//      (A, B);
+//   2. the chain threads (two channels of eight runs each) fold these, write the results into the
+//      shared memory of every block of the cluster, and fold what all blocks sent onto the state
+//      the turn began with: the state entering their own runs, and the one that the next turn
+//      begins with, which is thus known to every block without another exchange;
 //   3. the compute warps continue their runs from there and write the outputs.
-// Inputs are staged by bulk copies some turns ahead and read from memory once.  Everything is
-// folded in token order, so the results are the same bits on every run.
+// Inputs are staged some turns ahead and read from memory once; tokens behind the end and
+// channels beside a head are staged as zeros, which change nothing (e^0 = 1, x = 0).  Everything
+// is folded in token order, so the results are the same bits on every run.
+#include <type_traits>
+
 #include "efla_kernels.h"
 #include "efla_pages.cuh"
 #include "efla_scan.cuh"
+#include "efla_tma.cuh"
 #include "sm100.cuh"
 
 namespace efla {
@@ -40,79 +45,85 @@ __device__ __forceinline__ void st4(T* p, const P4& v) {
     store4(p, make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y));
 }
 
-constexpr int kTok = kScanChunk, kWarps = 8, kRun = kTok / kWarps, kCh = 128;
-constexpr int kComputeThreads = kWarps * 32, kChainThreads = kCh / 2, kThreads = kComputeThreads + kChainThreads;
-constexpr int kCluster = 16;       // most blocks of a cluster
-constexpr int kMarks = 8;          // chunks whose marks are kept
+constexpr int kValues = 4096, kWarps = 8, kRun = 4, kLanes4 = 128;      // values of a tile; channels x runs of a warp
+constexpr int kComputeThreads = kWarps * 32, kChainThreads = 64, kThreads = kComputeThreads + kChainThreads;
+constexpr int kCluster = 8;        // most blocks of a cluster
+constexpr int kMarks = 8;          // tiles whose marks are kept
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// How lanes map to (stream, channel): heads of d channels with 32 % (d / 4) == 0 are packed
-// side by side into a strip; other widths up to 128 take a strip each, wider ones several.
-struct Strips {
-    int dv;          // vectors of four channels per head
-    int heads;       // heads per strip
-    int per_head;    // strips per head
-    int count;       // strips
-    __host__ __device__ Strips(long Z, int d) {
-        dv = d / 4;
-        heads = dv <= 32 && 32 % dv == 0 ? 32 / dv : 1;
-        per_head = (dv + 31) / 32;
-        count = (int)(heads > 1 ? (Z + heads - 1) / heads : Z * per_head);
-    }
+// How streams, channels and tokens make strips and tiles: a function of the shape alone, since
+// the states kept for the backward pass lie by it.
+struct Geo {
+    int width;         // channels of a strip: 128, 64, 32
+    int groups;        // runs of a warp side by side: 128 / width
+    int tokens;        // of a tile: 32 groups
+    int heads;         // whole heads packed side by side in a strip (their width divides the strip's)
+    int per_head;      // strips of a head that is wider
+    int strips, steps;
+    int box;           // channels of one staged box: a head, or a strip's part of it
 };
 
-// What a lane holds of any strip.
+// What a lane holds: channels c .. c + 3 of stream z, run `run` of each tile.
 struct Lane {
-    int c, smem, row;     // channel within the head or its part; offset of token 0 in a staged tile; elements between tokens
-    int p, heads, per_head, d;
-    long Z;
-    __device__ __forceinline__ Lane(const Strips& S, long Z_, int d_, int lane)
-        : heads(S.heads), per_head(S.per_head), d(d_), Z(Z_) {
-        p = S.heads > 1 ? lane / S.dv : 0;
-        c = S.heads > 1 ? (lane % S.dv) * 4 : lane * 4;
-        row = S.per_head > 1 ? kCh : d_;
-        smem = S.heads > 1 ? p * kTok * d_ + c : c < row ? c : 0;       // off lanes: something that is there
-    }
-};
-struct Spot {
     long z;
-    int c;
+    int c, run;
     bool on;
+    int smem, row;     // element offset of the run's first token in a staged tile; elements between tokens
 };
-__device__ __forceinline__ Spot spot_of(const Lane& L, int strip) {
-    Spot s;
-    if (L.per_head == 1) {
-        s.z = (long)strip * L.heads + L.p;
-        s.c = L.c;
+__device__ __forceinline__ Lane lane_of(const Geo& G, long Z, int d, int strip, int warp, int lane) {
+    const int lanes = G.width / 4, dv = d / 4, q = lane % lanes;      // q: four channels of the strip
+    Lane L;
+    L.run = warp * G.groups + lane / lanes;
+    L.row = G.box;
+    if (G.heads > 1) {
+        const int p = q / dv;
+        L.z = (long)strip * G.heads + p;
+        L.c = (q % dv) * 4;
+        L.smem = p * G.tokens * d + L.c;
     } else {
-        s.z = strip / L.per_head;
-        s.c = (strip % L.per_head) * kCh + L.c;
+        L.z = strip / G.per_head;
+        L.c = (strip % G.per_head) * G.width + q * 4;
+        L.smem = q * 4 < G.box ? q * 4 : 0;
     }
-    s.on = s.z < L.Z && s.c < L.d;
-    return s;
+    L.on = L.z < Z && L.c < d;
+    L.smem += L.run * kRun * L.row;
+    return L;
 }
 
-// Stage one tensor's tile (one warp calls it; the barrier already expects the bytes).  A strip
-// that holds whole heads is `rows` x d contiguous elements per head; a part of a wide head is
-// copied token by token.  All addresses and sizes are multiples of 16 bytes, because d elements are.
-template <typename T>
-__device__ __forceinline__ void stage(T* dst, const T* src, const Strips& S, long Z, int Ttot, int d, int strip, int t0,
-                                      int rows, uint64_t* bar) {
-    const int lane = threadIdx.x & 31;
-    if (S.per_head == 1) {
-        const long z = (long)strip * S.heads + lane;
-        if (lane < S.heads && z < Z)
-            bulk_load(dst + lane * kTok * d, src + (z * Ttot + t0) * d, rows * d * (int)sizeof(T), bar);
-    } else {
-        const long z = strip / S.per_head;
-        const int c0 = (strip % S.per_head) * kCh;
-        for (int t = lane; t < rows; t += 32)
-            bulk_load(dst + t * kCh, src + (z * Ttot + t0 + t) * d + c0, min(kCh, d - c0) * (int)sizeof(T), bar);
-    }
+// Staging by one warp: bytes that will arrive, then each tensor's copies.  A strip of whole heads is
+// contiguous per head (one bulk copy each, about a tenth faster than TMA boxes); what lies behind
+// the end or beside the last head is zeroed.  A part of a wide head is a TMA box, which fills
+// with zeros itself.
+struct Tile {
+    int t0, rows, heads;      // tokens and heads that there are
+};
+__device__ __forceinline__ Tile tile_at(const Geo& G, long Z, int T, int strip, int chunk) {
+    Tile t;
+    t.t0 = chunk * G.tokens;
+    t.rows = min(G.tokens, T - t.t0);
+    t.heads = (int)min((long)G.heads, Z - (long)(strip / G.per_head) * G.heads);
+    return t;
 }
-__device__ __forceinline__ int strip_channels(const Strips& S, long Z, int d, int strip) {
-    if (S.heads > 1) return (int)min((long)S.heads, Z - (long)strip * S.heads) * d;
-    return S.per_head == 1 ? d : min(kCh, d - (strip % S.per_head) * kCh);
+__device__ __forceinline__ int tile_values(const Geo& G, const Tile& t) {
+    return G.per_head > 1 ? G.tokens * G.box : t.heads * t.rows * G.box;
+}
+template <typename T>
+__device__ __forceinline__ void zero_rest(T* dst, const Geo& G, const Tile& t) {
+    if (G.per_head > 1 || (t.rows == G.tokens && t.heads == G.heads)) return;
+    const int lane = threadIdx.x & 31, head = G.tokens * G.box, there = t.rows * G.box;
+    for (int p = 0; p < G.heads; ++p)
+        for (int i = (p < t.heads ? there : 0) + lane * 4; i < head; i += 128) st4(dst + p * head + i, all4(0.f));
+}
+template <typename T>
+__device__ __forceinline__ void stage(T* dst, const T* src, const CUtensorMap* map, const Geo& G, int Ttot, int strip,
+                                      const Tile& t, uint64_t* bar) {
+    const int lane = threadIdx.x & 31;
+    if (G.per_head > 1) {
+        if (lane == 0) tma_load_3d(dst, map, bar, (strip % G.per_head) * G.width, t.t0, strip / G.per_head);
+    } else if (lane < t.heads) {
+        const long z = (long)strip * G.heads + lane;
+        bulk_load(dst + lane * G.tokens * G.box, src + (z * Ttot + t.t0) * G.box, t.rows * G.box * (int)sizeof(T), bar);
+    }
 }
 
 // The packed sequence that holds token t: the largest n with cu[n] <= t.
@@ -127,17 +138,28 @@ __device__ __forceinline__ int seq_of(const ScanArgs& P, int t) {
     return lo;
 }
 
-// Which of a chunk's tokens begin or end a sequence (bit l: token l).  One warp calls it.
-__device__ __forceinline__ uint2 chunk_marks(const ScanArgs& P, int chunk) {
-    const int t0 = chunk * kTok;
-    if (!P.cu) return make_uint2(chunk == 0 ? 1u : 0u, P.T - t0 <= kTok ? 1u << (P.T - t0 - 1) : 0u);
-    static_assert(kTok == 32, "one lane per token");
-    const int t = t0 + (threadIdx.x & 31), n = t < P.T ? seq_of(P, t) : 0;
-    return make_uint2(__ballot_sync(0xffffffffu, t < P.T && P.cu[n] == t),
-                      __ballot_sync(0xffffffffu, t < P.T && P.cu[n + 1] == t + 1));
+// Which of a tile's tokens begin or end a sequence (bit l of word j: token 32 j + l), and whether any does.
+struct Marks {
+    uint32_t first[4], last[4];
+};
+struct MarkRing {
+    Marks m[kMarks];
+    uint32_t any[kMarks];
+};
+__device__ __forceinline__ void make_marks(const ScanArgs& P, const Geo& G, int chunk, MarkRing* ring, int slot) {
+    const int lane = threadIdx.x & 31;
+    uint32_t any = 0;
+    for (int j = 0; j < G.groups; ++j) {
+        const int t = chunk * G.tokens + 32 * j + lane, n = t < P.T ? seq_of(P, t) : 0;
+        const uint32_t first = __ballot_sync(0xffffffffu, t < P.T && (P.cu ? P.cu[n] == t : t == 0));
+        const uint32_t last = __ballot_sync(0xffffffffu, t < P.T && (P.cu ? P.cu[n + 1] : P.T) == t + 1);
+        if (lane == 0) ring->m[slot].first[j] = first, ring->m[slot].last[j] = last;
+        any |= first | last;
+    }
+    if (lane == 0) ring->any[slot] = any;
 }
-__device__ __forceinline__ uint32_t run_bits(uint32_t marks, int warp) {
-    return marks >> (warp * kRun) & ((1u << kRun) - 1u);
+__device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
+    return words[run >> 3] >> (run & 7) * kRun & ((1u << kRun) - 1u);
 }
 
 // Sequences without tokens pass their states through.
@@ -152,21 +174,38 @@ __device__ __forceinline__ void pass_empty(const ScanArgs& P, const float* in, f
 // A of a run with a sequence's begin in it: what came before does not matter, not even a NaN.
 // (No product of decays is -0.)  A cut is one for all channels.
 constexpr float kCut = -0.0f;
-__device__ __forceinline__ float2 run_on(float2 A, float2 h, float2 B) {
-    return __float_as_uint(A.x) == 0x80000000u ? B : fma2(A, h, B);
-}
+__device__ __forceinline__ bool is_cut(float A) { return __float_as_uint(A) == 0x80000000u; }
+__device__ __forceinline__ float2 run_on(float2 A, float2 h, float2 B) { return is_cut(A.x) ? B : fma2(A, h, B); }
 __device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
-// The state entering each run takes the place of its B.
+// Eight runs folded to one (A, B); the state entering each of them takes the place of its B.
+struct Fold {
+    float2 A, B;
+};
 template <bool kReverse>
-__device__ __forceinline__ void enter_runs(const float* runA, float* runB, float2 h) {
-    float2 A[kWarps], B[kWarps];
+__device__ __forceinline__ Fold fold_runs(const float* runA, const float* runB, int width) {
+    Fold f{both(1.f), both(0.f)};
+    bool cut = false;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) A[w] = ld2(runA + w * kCh), B[w] = ld2(runB + w * kCh);
+    for (int i = 0; i < 8; ++i) {
+        const int w = kReverse ? 7 - i : i;
+        const float2 a = ld2(runA + w * width);
+        cut |= is_cut(a.x);
+        f.B = run_on(a, f.B, ld2(runB + w * width));
+        f.A = mul2(f.A, a);
+    }
+    if (cut) f.A = both(kCut);
+    return f;
+}
+template <bool kReverse>
+__device__ __forceinline__ void enter_runs(const float* runA, float* runB, int width, float2 h) {
+    float2 A[8], B[8];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const int w = kReverse ? kWarps - 1 - i : i;
-        *reinterpret_cast<float2*>(runB + w * kCh) = h;
+    for (int w = 0; w < 8; ++w) A[w] = ld2(runA + w * width), B[w] = ld2(runB + w * width);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int w = kReverse ? 7 - i : i;
+        *reinterpret_cast<float2*>(runB + w * width) = h;
         h = run_on(A[w], h, B[w]);
     }
 }
@@ -205,41 +244,34 @@ __device__ __forceinline__ void wait_or_give_up(uint64_t* bar, int parity, bool*
     }
 }
 
-// A chain thread's part of one turn: the tile's (A, B) from its runs (kReverse: last run first; no
-// tile: nothing changes), the exchange, the state entering the tile; `carry` goes from this turn's
-// first state to the next one's.  sent: [2][rank][64] x {A, B of two channels}.
-template <bool kReverse>
-__device__ __forceinline__ float2 chain_turn(const float* runA, const float* runB, bool tile, int blocks, uint32_t rank,
-                                             int n, float4* sent, uint64_t* got, float2* carry, bool* dead,
-                                             uint32_t* err) {
-    float2 A = both(1.f), B = both(0.f);
-    if (tile) {
-        bool cut = false;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const int w = kReverse ? kWarps - 1 - i : i;
-            const float2 a = ld2(runA + w * kCh);
-            cut |= __float_as_uint(a.x) == 0x80000000u;
-            B = run_on(a, B, ld2(runB + w * kCh));
-            A = mul2(A, a);
-        }
-        if (cut) A = both(kCut);
-    }
+// A chain thread's part of one turn: it sends its eight runs' (A, B) to every block and folds
+// everybody's, in the order of time, onto `carry`, the state the turn began with, which becomes
+// the one the next turn begins with.  Returns the state entering its own runs.
+// sent: [2][blocks * groups][width / 2] x {A, B of two channels}; `entry`: its place in that order.
+__device__ __forceinline__ float2 chain_turn(const Fold& f, int blocks, const Geo& G, int entry, int pair, int n,
+                                             float4* sent, uint64_t* got, float2* carry, bool* dead, uint32_t* err) {
     float2 h = *carry;
-    if (blocks == 1) {
-        *carry = run_on(A, h, B);
+    const int entries = blocks * G.groups;
+    if (entries == 1) {
+        *carry = run_on(f.A, h, f.B);
         return h;
     }
-    const int k = threadIdx.x - kComputeThreads, buf = n & 1;
-    const uint32_t to = smem_u32(sent + (buf * blocks + rank) * kChainThreads + k), bar = smem_u32(got + buf);
-    for (int q = 0; q < blocks; ++q) send(in_block(to, q), in_block(bar, q), A, B);
-    if (k == 0) mbar_arrive_expect_tx(got + buf, blocks * kChainThreads * 16);
-    wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
+    const int buf = n & 1, row = G.width / 2;
+    float4* all = sent + buf * blocks * kChainThreads;
+    if (blocks == 1) {
+        all[entry * row + pair] = make_float4(f.A.x, f.A.y, f.B.x, f.B.y);
+        bar_sync(1, kChainThreads);
+    } else {
+        const uint32_t to = smem_u32(all + entry * row + pair), bar = smem_u32(got + buf);
+        for (int q = 0; q < blocks; ++q) send(in_block(to, q), in_block(bar, q), f.A, f.B);
+        if (threadIdx.x == kComputeThreads) mbar_arrive_expect_tx(got + buf, blocks * kChainThreads * 16);
+        wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
+    }
     float2 mine = h;
-    const float4* all = sent + buf * blocks * kChainThreads + k;
-    for (int q = 0; q < blocks; ++q) {
-        const float4 v = all[q * kChainThreads];
-        if (q == (int)rank) mine = h;
+#pragma unroll 4
+    for (int q = 0; q < entries; ++q) {
+        const float4 v = all[q * row + pair];
+        if (q == entry) mine = h;
         h = run_on(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
     }
     *carry = h;
@@ -274,31 +306,36 @@ __device__ __forceinline__ void token_gates(int rule, const float* gt, float gs,
     }
 }
 
-template <typename Tin, bool kShared>
-struct FwdSmem {
-    static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
-    static constexpr int kStage = kX + kG, kStages = 2;
-    static constexpr int kRuns = kWarps * kCh;                  // floats of one value of all runs
-    static constexpr int bytes(int blocks) { return kStages * kStage + 2 * kRuns * 4 + 2 * blocks * kChainThreads * 16 + 256; }
+// The staged tensors.
+struct Maps {
+    CUtensorMap x, g, dO;
 };
 
 template <typename Tin, bool kShared>
-__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, int blocks, int steps) {
+struct FwdSmem {
+    static constexpr int kX = kValues * sizeof(Tin), kG = kShared ? 0 : kValues * 4;
+    static constexpr int kStage = kX + kG, kStages = 2;
+    static constexpr int kRuns = kWarps * kLanes4;              // floats of one value of all runs
+    static constexpr int bytes(int blocks) {
+        return kStages * kStage + 2 * kRuns * 4 + 2 * blocks * kChainThreads * 16 + 64 + (int)sizeof(MarkRing);
+    }
+};
+
+template <typename Tin, bool kShared>
+__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const __grid_constant__ Maps maps, Geo G,
+                                                               int blocks) {
     using M = FwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
-    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [A, B (then: entering)][warp][128]
+    float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [A, B (then: entering)][run][width]
     float4* sent = reinterpret_cast<float4*>(runs + 2 * M::kRuns);
     uint64_t* full = reinterpret_cast<uint64_t*>(sent + 2 * blocks * kChainThreads);
     uint64_t* ready = full + M::kStages;      // the tile's (A, B) of all runs are there
     uint64_t* entered = ready + 1;            // the states entering them are
     uint64_t* got = entered + 1;              // [2] all blocks' (A, B) are
-    uint2* marks = reinterpret_cast<uint2*>(got + 2);
-    const Strips S(P.Z, P.d);
+    MarkRing* ring = reinterpret_cast<MarkRing*>(full + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
-    const int strip = blockIdx.x / blocks, turns = (steps + blocks - 1) / blocks;
-    const Tin* x = static_cast<const Tin*>(P.x);
-    Tin* o = static_cast<Tin*>(P.o);
+    const int rank = blocks > 1 ? (int)cluster_rank() : 0;
+    const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
     if (threadIdx.x == 0) {
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
         mbar_init(ready, kWarps);
@@ -310,17 +347,19 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, int b
     __syncthreads();
     auto prefetch = [&](int n) {      // by the last warp
         const int chunk = n * blocks + rank;
-        if (chunk >= steps) return;
-        const int st = n % M::kStages, t0 = chunk * kTok, rows = min(kTok, P.T - t0);
-        const uint2 m = chunk_marks(P, chunk);
-        if (lane == 0) {
-            marks[n % kMarks] = m;
-            mbar_arrive_expect_tx(full + st, rows * strip_channels(S, P.Z, P.d, strip) * (int)(sizeof(Tin) + (kShared ? 0 : 4)));
-        }
+        if (chunk >= G.steps) return;
+        const int st = n % M::kStages;
+        const Tile t = tile_at(G, P.Z, P.T, strip, chunk);
+        Tin* dx = reinterpret_cast<Tin*>(smem + st * M::kStage);
+        float* dg = reinterpret_cast<float*>(smem + st * M::kStage + M::kX);
+        make_marks(P, G, chunk, ring, n % kMarks);
+        zero_rest(dx, G, t);
+        if (!kShared) zero_rest(dg, G, t);
         __syncwarp();
-        char* dst = smem + st * M::kStage;
-        stage(reinterpret_cast<Tin*>(dst), x, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
-        if (!kShared) stage(reinterpret_cast<float*>(dst + M::kX), P.g, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
+        if (lane == 0) mbar_arrive_expect_tx(full + st, tile_values(G, t) * (int)(sizeof(Tin) + (kShared ? 0 : 4)));
+        __syncwarp();
+        stage(dx, static_cast<const Tin*>(P.x), &maps.x, G, P.T, strip, t, full + st);
+        if (!kShared) stage(dg, P.g, &maps.g, G, P.T, strip, t, full + st);
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
@@ -329,97 +368,88 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, int b
     bool dead = false;
 
     if (warp >= kWarps) {                 // the chain
-        const int k = (threadIdx.x - kComputeThreads) * 2;
+        const int k = threadIdx.x - kComputeThreads, pair = k % (G.width / 2), part = k / (G.width / 2);
+        float* runA = runs + part * 8 * G.width + pair * 2;
+        float* runB = runA + M::kRuns;
         float2 carry = both(0.f);
         for (int n = 0; n < turns; ++n) {
             const int chunk = n * blocks + rank;
-            const bool tile = chunk < steps;
+            const bool tile = chunk < G.steps;
+            Fold f{both(1.f), both(0.f)};
             if (tile) {
                 wait_or_give_up(ready, n & 1, &dead, P.err);
-                if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);      // the stage has been read
+                f = fold_runs<false>(runA, runB, G.width);
             }
-            const float2 h = chain_turn<false>(runs + k, runs + M::kRuns + k, tile, blocks, rank, n, sent, got, &carry,
-                                               &dead, P.err);
+            if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);      // the stage has been read
+            const float2 h = chain_turn(f, blocks, G, rank * G.groups + part, pair, n, sent, got, &carry, &dead, P.err);
             if (tile) {
-                enter_runs<false>(runs + k, runs + M::kRuns + k, h);
+                enter_runs<false>(runA, runB, G.width, h);
                 warp_arrive(entered);
-                if (P.E) *reinterpret_cast<float2*>(P.E + ((size_t)chunk * S.count + strip) * kCh + k) = h;
+                if (P.E && part == 0)
+                    *reinterpret_cast<float2*>(P.E + ((size_t)chunk * G.strips + strip) * G.width + pair * 2) = h;
             }
         }
     } else {
-        const Lane lanes(S, P.Z, P.d, lane);
-        const Spot L = spot_of(lanes, strip);
-        const int mine = lanes.smem + warp * kRun * lanes.row;
-        float* run = runs + warp * kCh + lane * 4;
+        const Lane L = lane_of(G, P.Z, P.d, strip, warp, lane);
+        float* run = runs + warp * kLanes4 + lane * 4;
+        const Tin* x0 = reinterpret_cast<const Tin*>(smem) + L.smem;
+        const float* g0 = reinterpret_cast<const float*>(smem + M::kX) + L.smem;
         for (int n = 0; n < turns; ++n) {
             const int chunk = n * blocks + rank;
-            if (chunk >= steps) break;
-            const int tw = chunk * kTok + warp * kRun, st = n % M::kStages;
+            if (chunk >= G.steps) break;
+            const int tw = chunk * G.tokens + L.run * kRun, st = n % M::kStages;
+            const int live = L.on ? P.T - tw : 0;
             float gs[kRun];
             if (kShared) {
 #pragma unroll
-                for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
+                for (int i = 0; i < kRun; ++i) gs[i] = i < live ? P.g[L.z * P.T + tw + i] : 0.f;
             }
             wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
-            const uint2 m = marks[n % kMarks];
-            const uint32_t first = run_bits(m.x, warp);
-            const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + mine;
-            const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + M::kX) + mine;
-            // 1. the run's tokens as h = a h' + b, and the run's (A, B)
-            Gate<kShared> a;
-            P4 b[kRun];
+            const Tin* xs = x0 + st * (M::kStage / (int)sizeof(Tin));
+            const float* gt = g0 + st * (M::kStage / 4);
+            // most tiles have no begin or end of a sequence in them; their code knows it, and the rule
+            auto tile = [&](auto plain_, auto rule_) {
+                constexpr bool plain = decltype(plain_)::value;
+                const int rule = decltype(rule_)::value < 0 ? P.rule : decltype(rule_)::value;
+                const uint32_t first = plain ? 0u : run_bits(ring->m[n % kMarks].first, L.run);
+                // 1. the run's tokens as h = a h' + b, and the run's (A, B)
+                Gate<kShared> a;
+                P4 b[kRun], ra = all4(1.f), rb = all4(0.f);
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                P4 a1, w, dw;
-                token_gates<kShared, false>(P.rule, gt + i * lanes.row, gs[i], &a1, &w, &dw);
-                a.set(i, a1);
-                b[i] = mul4(w, ld4(xs + i * lanes.row));
-            }
-            if (tw + kRun > P.T) {            // behind the end: tokens that change nothing
-#pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    if (tw + i >= P.T) {
-                        a.set(i, all4(1.f));
-                        b[i] = all4(0.f);
+                for (int i = 0; i < kRun; ++i) {
+                    P4 a1, w, dw;
+                    token_gates<kShared, false>(rule, gt + i * L.row, gs[i], &a1, &w, &dw);
+                    b[i] = mul4(w, ld4(xs + i * L.row));
+                    if (!plain && (first >> i & 1u)) {       // a sequence begins: its own state enters, no other
+                        if (P.S0 && L.on)
+                            b[i] = fma4(a1, ld4(P.S0 + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c), b[i]);
+                        a1 = rb = all4(0.f);
                     }
-            }
-            for (uint32_t bits = first; bits; bits &= bits - 1) {     // a sequence begins: its own state enters
-                const int from = __ffs(bits) - 1;
-                const P4 s0 = P.S0 && L.on ? ld4(P.S0 + ((long)seq_of(P, tw + from) * P.Z + L.z) * P.d + L.c) : all4(0.f);
-#pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    if (i == from) {
-                        b[i] = fma4(a.at(i), s0, b[i]);
-                        a.set(i, all4(0.f));
-                    }
-            }
-            P4 ra = all4(1.f), rb = all4(0.f);
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                if (first >> i & 1u) rb = all4(0.f);
-                ra = mul4(ra, a.at(i));
-                rb = fma4(a.at(i), rb, b[i]);
-            }
-            if (first) ra = all4(kCut);
-            st4(run, ra);
-            st4(run + M::kRuns, rb);
-            warp_arrive(ready);
-            // 3. the outputs
-            wait_or_give_up(entered, n & 1, &dead, P.err);
-            P4 h = ld4(run + M::kRuns);
-            const uint32_t last = P.S_T ? run_bits(m.y, warp) : 0u;
-            const int live = L.on ? P.T - tw : 0;
-            if (!o && !last) continue;
-            Tin* out = o + (L.z * P.T + tw) * P.d + L.c;
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                if (first >> i & 1u) h = all4(0.f);          // its state is in b
-                h = fma4(a.at(i), h, b[i]);
-                if (o && i < live) st4(out + i * P.d, h);
-                if (last >> i & 1u) {                        // a sequence ends
-                    if (L.on) st4(P.S_T + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, h);
+                    a.set(i, a1);
+                    ra = mul4(ra, a1);
+                    rb = fma4(a1, rb, b[i]);
                 }
-            }
+                if (!plain && first) ra = all4(kCut);
+                st4(run, ra);
+                st4(run + M::kRuns, rb);
+                warp_arrive(ready);
+                // 3. the outputs
+                wait_or_give_up(entered, n & 1, &dead, P.err);
+                P4 h = ld4(run + M::kRuns);
+                Tin* out = static_cast<Tin*>(P.o) + (L.z * P.T + tw) * P.d + L.c;
+                const uint32_t last = plain || !P.S_T ? 0u : run_bits(ring->m[n % kMarks].last, L.run);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    if (!plain && (first >> i & 1u)) h = all4(0.f);      // its state is in b
+                    h = fma4(a.at(i), h, b[i]);
+                    if (P.o && i < live) st4(out + i * P.d, h);
+                    if (!plain && (last >> i & 1u) && L.on)
+                        st4(P.S_T + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, h);
+                }
+            };
+            if (ring->any[n % kMarks]) tile(std::false_type(), std::integral_constant<int, -1>());
+            else if (P.rule == kRuleExact) tile(std::true_type(), std::integral_constant<int, kRuleExact>());
+            else tile(std::true_type(), std::integral_constant<int, kRuleEuler>());
         }
     }
     if (blocks > 1) cluster_sync();       // no block leaves while another may still send to it
@@ -428,35 +458,36 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, int b
 // The reverse pass.  c = e^{g_t} G_t flows from token t into t - 1 (dS_T into a sequence's last
 // token), G_t = dO_t + c: affine again, c_out = A c_in + R over a run, and the tiles are taken
 // from the last to the first.  A tile's own states are put together again from the state that
-// the forward kept for it, so no state but one of 32 tokens is ever stored.
+// the forward kept for it, so no other state is ever stored.
 template <typename Tin, bool kShared>
 struct BwdSmem {
-    static constexpr int kX = kTok * kCh * sizeof(Tin), kG = kShared ? 0 : kTok * kCh * 4;
+    static constexpr int kX = kValues * sizeof(Tin), kG = kShared ? 0 : kValues * 4;
     static constexpr int kStage = 2 * kX + kG, kStages = 2;
-    static constexpr int kRuns = kWarps * kCh;
-    static constexpr int bytes(int blocks) { return kStages * kStage + 4 * kRuns * 4 + 2 * blocks * kChainThreads * 16 + 256; }
+    static constexpr int kRuns = kWarps * kLanes4;
+    static constexpr int bytes(int blocks) {
+        return kStages * kStage + 4 * kRuns * 4 + 2 * blocks * kChainThreads * 16 + kChainThreads * 16 + 64 +
+               (int)sizeof(MarkRing);
+    }
 };
 
 template <typename Tin, bool kShared>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const float* states, float* parts, int blocks,
-                                                               int steps) {
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const __grid_constant__ Maps maps, Geo G,
+                                                               int blocks) {
     using M = BwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
-    // [A, B (then: the state entering), reverse A, R (then: the flow entering)][warp][128]
+    // [A, B (then: the state entering), reverse A, R (then: the flow entering)][run][width]
     float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);
     float4* sent = reinterpret_cast<float4*>(runs + 4 * M::kRuns);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sent + 2 * blocks * kChainThreads);
+    float4* folds = sent + 2 * blocks * kChainThreads;      // the parts' forward (A, B)
+    uint64_t* full = reinterpret_cast<uint64_t*>(folds + kChainThreads);
     uint64_t* spent = full + M::kStages;      // a stage has been read to its end
     uint64_t* ready = spent + M::kStages;
     uint64_t* entered = ready + 1;
     uint64_t* got = entered + 1;
-    uint2* marks = reinterpret_cast<uint2*>(got + 2);
-    const Strips S(P.Z, P.d);
+    MarkRing* ring = reinterpret_cast<MarkRing*>(full + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
-    const int strip = blockIdx.x / blocks, turns = (steps + blocks - 1) / blocks;
-    const Tin* x = static_cast<const Tin*>(P.x);
-    const Tin* dO = static_cast<const Tin*>(P.dO);
+    const int rank = blocks > 1 ? (int)cluster_rank() : 0;
+    const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
     if (threadIdx.x == 0) {
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1), mbar_init(spent + i, kWarps);
         mbar_init(ready, kWarps);
@@ -467,20 +498,22 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     }
     __syncthreads();
     auto prefetch = [&](int n) {
-        const int chunk = steps - 1 - (n * blocks + (int)rank);
+        const int chunk = G.steps - 1 - (n * blocks + rank);
         if (chunk < 0) return;
-        const int st = n % M::kStages, t0 = chunk * kTok, rows = min(kTok, P.T - t0);
-        const uint2 m = chunk_marks(P, chunk);
-        if (lane == 0) {
-            marks[n % kMarks] = m;
-            mbar_arrive_expect_tx(full + st,
-                                  rows * strip_channels(S, P.Z, P.d, strip) * (int)(2 * sizeof(Tin) + (kShared ? 0 : 4)));
-        }
+        const int st = n % M::kStages;
+        const Tile t = tile_at(G, P.Z, P.T, strip, chunk);
+        Tin* sx = reinterpret_cast<Tin*>(smem + st * M::kStage);
+        float* sg = reinterpret_cast<float*>(smem + st * M::kStage + 2 * M::kX);
+        make_marks(P, G, chunk, ring, n % kMarks);
+        zero_rest(sx, G, t);
+        zero_rest(sx + kValues, G, t);
+        if (!kShared) zero_rest(sg, G, t);
         __syncwarp();
-        char* dst = smem + st * M::kStage;
-        stage(reinterpret_cast<Tin*>(dst), x, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
-        stage(reinterpret_cast<Tin*>(dst + M::kX), dO, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
-        if (!kShared) stage(reinterpret_cast<float*>(dst + 2 * M::kX), P.g, S, P.Z, P.T, P.d, strip, t0, rows, full + st);
+        if (lane == 0) mbar_arrive_expect_tx(full + st, tile_values(G, t) * (int)(2 * sizeof(Tin) + (kShared ? 0 : 4)));
+        __syncwarp();
+        stage(sx, static_cast<const Tin*>(P.x), &maps.x, G, P.T, strip, t, full + st);
+        stage(sx + kValues, static_cast<const Tin*>(P.dO), &maps.dO, G, P.T, strip, t, full + st);
+        if (!kShared) stage(sg, P.g, &maps.g, G, P.T, strip, t, full + st);
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
@@ -489,21 +522,36 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     bool dead = false;
 
     if (warp >= kWarps) {             // the chain
-        const int k = (threadIdx.x - kComputeThreads) * 2;
+        const int k = threadIdx.x - kComputeThreads, pair = k % (G.width / 2), part = k / (G.width / 2);
+        float* runA = runs + part * 8 * G.width + pair * 2;
+        float* runB = runA + M::kRuns;
+        float* revA = runB + M::kRuns;
+        float* revB = revA + M::kRuns;
         float2 carry = both(0.f);
         for (int n = 0; n < turns; ++n) {
-            const int chunk = steps - 1 - (n * blocks + (int)rank);
+            const int chunk = G.steps - 1 - (n * blocks + rank);
             const bool tile = chunk >= 0;
             float2 h = both(0.f);
+            Fold f{both(1.f), both(0.f)};
             if (tile) {
-                if (chunk > 0) h = ld2(states + ((size_t)chunk * S.count + strip) * kCh + k);
+                if (chunk > 0) h = ld2(P.E + ((size_t)chunk * G.strips + strip) * G.width + pair * 2);
                 wait_or_give_up(ready, n & 1, &dead, P.err);
+                f = fold_runs<true>(revA, revB, G.width);
             }
-            const float2 c = chain_turn<true>(runs + 2 * M::kRuns + k, runs + 3 * M::kRuns + k, tile, blocks, rank, n, sent,
-                                              got, &carry, &dead, P.err);
+            const float2 c = chain_turn(f, blocks, G, rank * G.groups + G.groups - 1 - part, pair, n, sent, got, &carry,
+                                        &dead, P.err);
             if (tile) {
-                enter_runs<true>(runs + 2 * M::kRuns + k, runs + 3 * M::kRuns + k, c);
-                enter_runs<false>(runs + k, runs + M::kRuns + k, h);
+                if (G.groups > 1) {       // the state entering this part, by the parts before it
+                    const Fold own = fold_runs<false>(runA, runB, G.width);
+                    folds[k] = make_float4(own.A.x, own.A.y, own.B.x, own.B.y);
+                    bar_sync(1, kChainThreads);
+                    for (int p = 0; p < part; ++p) {
+                        const float4 v = folds[p * (G.width / 2) + pair];
+                        h = run_on(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
+                    }
+                }
+                enter_runs<true>(revA, revB, G.width, c);
+                enter_runs<false>(runA, runB, G.width, h);
                 warp_arrive(entered);
                 if (warp == kThreads / 32 - 1 && chunk - M::kStages * blocks >= 0) {
                     wait_or_give_up(spent + n % M::kStages, n / M::kStages & 1, &dead, P.err);
@@ -512,136 +560,101 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
             }
         }
     } else {
-        const Lane lanes(S, P.Z, P.d, lane);
-        const Spot L = spot_of(lanes, strip);
-        const int mine = lanes.smem + warp * kRun * lanes.row;
+        const Lane L = lane_of(G, P.Z, P.d, strip, warp, lane);
+        float* run = runs + warp * kLanes4 + lane * 4;
+        const Tin* x0 = reinterpret_cast<const Tin*>(smem) + L.smem;
+        const float* g0 = reinterpret_cast<const float*>(smem + 2 * M::kX) + L.smem;
+        float* parts = static_cast<float*>(P.scratch);
         for (int n = 0; n < turns; ++n) {
-            const int chunk = steps - 1 - (n * blocks + (int)rank);
+            const int chunk = G.steps - 1 - (n * blocks + rank);
             if (chunk < 0) break;
-            const int tw = chunk * kTok + warp * kRun, st = n % M::kStages;
-            const bool ragged = tw + kRun > P.T;
+            const int tw = chunk * G.tokens + L.run * kRun, st = n % M::kStages;
+            const int live = L.on ? P.T - tw : 0;
             float gs[kRun];
             if (kShared) {
-    #pragma unroll
-                for (int i = 0; i < kRun; ++i) gs[i] = L.on && tw + i < P.T ? P.g[L.z * P.T + tw + i] : 0.f;
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) gs[i] = i < live ? P.g[L.z * P.T + tw + i] : 0.f;
             }
             wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
-            const uint2 m = marks[n % kMarks];
-            const uint32_t first = run_bits(m.x, warp), last = run_bits(m.y, warp);
-            const int off = mine;
-            const Tin* xs = reinterpret_cast<const Tin*>(smem + st * M::kStage) + off;
-            const Tin* us = reinterpret_cast<const Tin*>(smem + st * M::kStage + M::kX) + off;
-            const float* gt = reinterpret_cast<const float*>(smem + st * M::kStage + 2 * M::kX) + off;
-            auto row_of = [&](int i) { return ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c; };
-            auto row = [&](const float* from, int i) { return from && L.on ? ld4(from + row_of(i)) : all4(0.f); };
-            // 1. the gates, and the run's (A, B) forward and in reverse
-            Gate<kShared> a, w, dw;
-    #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                P4 a1, w1, dw1;
-                token_gates<kShared, true>(P.rule, gt + i * lanes.row, gs[i], &a1, &w1, &dw1);
-                if (ragged && tw + i >= P.T) a1 = all4(1.f), w1 = dw1 = all4(0.f);
-                a.set(i, a1);
-                w.set(i, w1);
-                dw.set(i, dw1);
-            }
-            // (tokens behind the end are staged as whatever the stage held)
-            auto x_at = [&](int i) { return ragged && tw + i >= P.T ? all4(0.f) : ld4(xs + i * lanes.row); };
-            auto u_at = [&](int i) { return ragged && tw + i >= P.T ? all4(0.f) : ld4(us + i * lanes.row); };
-            const int cut = 31 - __clz(first);         // the last begin in the run; -1: none
-            P4 ra = all4(1.f), rb = all4(0.f), edge = all4(0.f);
-            if (first) edge = row(P.S0, cut);
-    #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                if (i == cut) rb = edge;
-                ra = mul4(ra, a.at(i));
-                rb = fma4(a.at(i), rb, mul4(w.at(i), x_at(i)));
-            }
-            if (first) ra = all4(kCut);
-            float* out = runs + warp * kCh + lane * 4;
-            st4(out, ra);
-            st4(out + M::kRuns, rb);
-            ra = all4(1.f);
-            rb = all4(0.f);
-            const int stop = __ffs(last) - 1;          // the first end in the run
-            if (last) edge = row(P.dST, stop);
-    #pragma unroll
-            for (int i = kRun - 1; i >= 0; --i) {
-                if (i == stop) rb = edge;
-                ra = mul4(ra, a.at(i));
-                rb = mul4(a.at(i), add4(u_at(i), rb));
-            }
-            if (last) ra = all4(kCut);
-            st4(out + 2 * M::kRuns, ra);
-            st4(out + 3 * M::kRuns, rb);
-            warp_arrive(ready);
-            wait_or_give_up(entered, n & 1, &dead, P.err);
-            // 2. the states before the run's tokens: e = a h' + w' x
-            P4 e[kRun], G[kRun];
-            P4 h = ld4(out + M::kRuns);
-    #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                const P4 xv = x_at(i);
-                e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
-                h = fma4(a.at(i), h, mul4(w.at(i), xv));
-            }
-            for (uint32_t bits = first; bits; bits &= bits - 1) {       // once more from where a sequence begins
-                const int from = __ffs(bits) - 1;
-                h = row(P.S0, from);
-    #pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    if (i >= from) {
-                        const P4 xv = x_at(i);
-                        e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
-                        h = fma4(a.at(i), h, mul4(w.at(i), xv));
-                    }
-            }
-            // 3. the gradients
-            P4 c = ld4(out + 3 * M::kRuns);
-    #pragma unroll
-            for (int i = kRun - 1; i >= 0; --i) {
-                G[i] = add4(u_at(i), c);
-                c = mul4(a.at(i), G[i]);
-            }
-            for (uint32_t bits = last; bits;) {                         // once more from where a sequence ends
-                const int from = 31 - __clz(bits);
-                bits ^= 1u << from;
-                c = row(P.dST, from);
-    #pragma unroll
-                for (int i = kRun - 1; i >= 0; --i)
-                    if (i <= from) {
-                        G[i] = add4(u_at(i), c);
-                        c = mul4(a.at(i), G[i]);
-                    }
-            }
-            const int live = L.on ? P.T - tw : 0;
-            float* dx = P.dx + (L.z * P.T + tw) * P.d + L.c;
-            float* dg = P.dg + (L.z * P.T + tw) * (kShared ? 1 : P.d) + (kShared ? 0 : L.c);
-    #pragma unroll
-            for (int i = 0; i < kRun; ++i) {
-                const P4 dgv = mul4(e[i], G[i]);
-                if (i < live) {
-                    st4(dx + i * P.d, mul4(w.at(i), G[i]));
-                    if (!kShared) st4(dg + i * P.d, dgv);
+            const Tin* xs = x0 + st * (M::kStage / (int)sizeof(Tin));
+            const Tin* us = xs + kValues;
+            const float* gt = g0 + st * (M::kStage / 4);
+            auto tile = [&](auto plain_, auto rule_) {
+                constexpr bool plain = decltype(plain_)::value;
+                const int rule = decltype(rule_)::value < 0 ? P.rule : decltype(rule_)::value;
+                const uint32_t first = plain ? 0u : run_bits(ring->m[n % kMarks].first, L.run);
+                const uint32_t last = plain ? 0u : run_bits(ring->m[n % kMarks].last, L.run);
+                auto row_of = [&](int i) { return ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c; };
+                auto row = [&](const float* from, int i) { return from && L.on ? ld4(from + row_of(i)) : all4(0.f); };
+                // 1. the gates, and the run's (A, B) forward and in reverse
+                Gate<kShared> a, w, dw;
+                P4 ra = all4(1.f), rb = all4(0.f);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    P4 a1, w1, dw1;
+                    token_gates<kShared, true>(rule, gt + i * L.row, gs[i], &a1, &w1, &dw1);
+                    a.set(i, a1);
+                    w.set(i, w1);
+                    dw.set(i, dw1);
+                    if (!plain && (first >> i & 1u)) rb = row(P.S0, i);
+                    ra = mul4(ra, a1);
+                    rb = fma4(a1, rb, mul4(w1, ld4(xs + i * L.row)));
                 }
-                if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
-                    float sum = i < live ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
-                    for (int far = S.heads > 1 ? S.dv / 2 : 16; far > 0; far >>= 1)
-                        sum += __shfl_xor_sync(0xffffffffu, sum, far);
-                    if (i < live && (S.heads > 1 ? lane % S.dv == 0 : lane == 0)) {
-                        if (S.per_head == 1) dg[i] = sum;
-                        else parts[((long)(strip % S.per_head) * P.Z + L.z) * P.T + tw + i] = sum;
-                    }
+                if (!plain && first) ra = all4(kCut);
+                st4(run, ra);
+                st4(run + M::kRuns, rb);
+                ra = all4(1.f);
+                rb = all4(0.f);
+#pragma unroll
+                for (int i = kRun - 1; i >= 0; --i) {
+                    if (!plain && (last >> i & 1u)) rb = row(P.dST, i);
+                    ra = mul4(ra, a.at(i));
+                    rb = mul4(a.at(i), add4(ld4(us + i * L.row), rb));
                 }
-            }
-            for (uint32_t bits = P.dS0 ? first : 0u; bits; bits &= bits - 1) {
-                const int from = __ffs(bits) - 1;
-                P4 d0 = all4(0.f);
-    #pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    if (i == from) d0 = mul4(a.at(i), G[i]);
-                if (L.on) st4(P.dS0 + row_of(from), d0);
-            }
+                if (!plain && last) ra = all4(kCut);
+                st4(run + 2 * M::kRuns, ra);
+                st4(run + 3 * M::kRuns, rb);
+                warp_arrive(ready);
+                wait_or_give_up(entered, n & 1, &dead, P.err);
+                // 2. the states before the run's tokens: e = a h' + w' x
+                P4 e[kRun];
+                P4 h = ld4(run + M::kRuns);
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    if (!plain && (first >> i & 1u)) h = row(P.S0, i);
+                    const P4 xv = ld4(xs + i * L.row);
+                    e[i] = fma4(a.at(i), h, mul4(dw.at(i), xv));
+                    h = fma4(a.at(i), h, mul4(w.at(i), xv));
+                }
+                // 3. the gradients
+                P4 c = ld4(run + 3 * M::kRuns);
+                float* dx = P.dx + (L.z * P.T + tw) * P.d + L.c;
+                float* dg = P.dg + (L.z * P.T + tw) * (kShared ? 1 : P.d) + (kShared ? 0 : L.c);
+#pragma unroll
+                for (int i = kRun - 1; i >= 0; --i) {
+                    if (!plain && (last >> i & 1u)) c = row(P.dST, i);
+                    const P4 Gt = add4(ld4(us + i * L.row), c);
+                    const P4 dgv = mul4(e[i], Gt);
+                    c = mul4(a.at(i), Gt);
+                    if (i < live) {
+                        st4(dx + i * P.d, mul4(w.at(i), Gt));
+                        if (!kShared) st4(dg + i * P.d, dgv);
+                    }
+                    if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
+                        float sum = i < live ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
+                        const int span = G.heads > 1 ? P.d / 4 : G.width / 4;
+                        for (int far = span / 2; far > 0; far >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, far);
+                        if (i < live && lane % span == 0) {
+                            if (G.per_head == 1) dg[i] = sum;
+                            else parts[((long)(strip % G.per_head) * P.Z + L.z) * P.T + tw + i] = sum;
+                        }
+                    }
+                    if (!plain && P.dS0 && (first >> i & 1u) && L.on) st4(P.dS0 + row_of(i), c);
+                }
+            };
+            if (ring->any[n % kMarks]) tile(std::false_type(), std::integral_constant<int, -1>());
+            else if (P.rule == kRuleExact) tile(std::true_type(), std::integral_constant<int, kRuleExact>());
+            else tile(std::true_type(), std::integral_constant<int, kRuleEuler>());
             warp_arrive(spent + st);
         }
     }
@@ -682,29 +695,56 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Tin* __restrict__ 
     st4(o + row + j, h);
 }
 
+// ---------------------------------------------------------------- host
+// The widest strips that still give every SM something to do (48 strips with clusters of up to
+// eight blocks), leave at most a quarter of the lanes without a channel, and a tile of which is
+// not longer than the sequence; or the best that can be had of these.
+Geo scan_geo(long Z, int T, int d) {
+    Geo best{};
+    double most = -1;
+    for (int groups = 1; groups <= 4; groups *= 2) {
+        Geo G;
+        G.groups = groups;
+        G.width = kLanes4 / groups;
+        G.tokens = 32 * groups;
+        G.heads = d < G.width && G.width % d == 0 ? G.width / d : 1;
+        G.per_head = (d + G.width - 1) / G.width;
+        G.strips = (int)(G.heads > 1 ? (Z + G.heads - 1) / G.heads : Z * G.per_head);
+        G.steps = (int)(((long)T + G.tokens - 1) / G.tokens);
+        G.box = d < G.width ? d : G.width;
+        const double used = (double)Z * d / ((double)G.strips * G.width), fill = G.strips < 48 ? G.strips / 48.0 : 1.0;
+        if (groups > 1 && T <= G.tokens / 2) break;
+        if (used * fill > most + 1e-9) best = G, most = used * fill;
+        if (used >= 0.75 && fill >= 1.0) break;
+    }
+    return best;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 }  // namespace
 
-static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-static long scan_steps(int T) { return ((long)T + kTok - 1) / kTok; }
-
-size_t scan_states_bytes(long Z, int T, int d) { return (size_t)scan_steps(T) * Strips(Z, d).count * kCh * sizeof(float); }
+size_t scan_states_bytes(long Z, int T, int d) {
+    const Geo G = scan_geo(Z, T, d);
+    return up256((size_t)G.steps * G.strips * G.width * sizeof(float));
+}
 // the partial sums of a shared decay's gradient where a head is wider than a strip
 size_t scan_scratch_bytes(long Z, int T, int d, int gw, bool backward) {
-    const Strips S(Z, d);
-    return backward && gw == 1 && S.per_head > 1 ? up256((size_t)S.per_head * Z * T * sizeof(float)) : 0;
+    const Geo G = scan_geo(Z, T, d);
+    return backward && gw == 1 && G.per_head > 1 ? up256((size_t)G.per_head * Z * T * sizeof(float)) : 0;
 }
 
 namespace {
 
 // How many clusters of each size a device holds at once, asked once per device and kernel.
 struct Room {
-    std::atomic<int> clusters[5];      // of 1, 2, 4, 8, 16 blocks
+    std::atomic<int> clusters[kCluster + 1];
     std::atomic<int> sms;
 };
 
 template <typename Kernel>
-cudaError_t config(Kernel kernel, int blocks, int smem, long strips, cudaStream_t stream, cudaLaunchConfig_t* cfg,
-                   cudaLaunchAttribute* attr) {
+void config(Kernel, int blocks, int smem, long strips, cudaStream_t stream, cudaLaunchConfig_t* cfg,
+            cudaLaunchAttribute* attr) {
     *cfg = cudaLaunchConfig_t{};
     cfg->gridDim = dim3((unsigned)(strips * blocks));
     cfg->blockDim = dim3(kThreads);
@@ -715,7 +755,6 @@ cudaError_t config(Kernel kernel, int blocks, int smem, long strips, cudaStream_
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg->attrs = attr;
     cfg->numAttrs = blocks > 1 ? 1 : 0;
-    return cudaSuccess;
 }
 
 template <typename Kernel>
@@ -725,77 +764,94 @@ cudaError_t find_room(Kernel kernel, int (*smem)(int), Room* room) {
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(kCluster))) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-    for (int i = 0; i < 5; ++i) {
+    for (int b = 1; b <= kCluster; ++b) {
         int n = 0;
-        if (i == 0) {
+        if (b == 1) {
             if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem(1))) != cudaSuccess) return e;
             n *= sms;
         } else {
             cudaLaunchConfig_t cfg;
             cudaLaunchAttribute attr[1];
-            config(kernel, 1 << i, smem(1 << i), 64, nullptr, &cfg, attr);
+            config(kernel, b, smem(b), 64, nullptr, &cfg, attr);
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
                 cudaGetLastError();       // a size that this device does not run
                 n = 0;
             }
         }
-        room->clusters[i].store(n, std::memory_order_relaxed);
+        room->clusters[b].store(n, std::memory_order_relaxed);
     }
     room->sms.store(sms, std::memory_order_release);
     return cudaSuccess;
 }
 
-// Blocks per cluster: with rounds = strips / clusters held at once, a strip's turns are
-// ceil(steps / blocks), and a turn takes as long as the blocks that share an SM, or, for fewer
-// than two, as its own latency (about 1.6 of a block's share at full rate).
+// Blocks per cluster: a strip takes ceil(steps / blocks) turns, in as many rounds as the device
+// needs to hold all strips' clusters; a turn takes as long as the blocks that share an SM need,
+// and with fewer than two of them its own latency.
 int pick_blocks(const Room& room, long strips, long steps) {
     int best = 1;
     double least = 0;
-    for (int i = 0; i < 5; ++i) {
-        const int n = room.clusters[i].load(std::memory_order_relaxed), blocks = 1 << i;
-        if (n == 0 || (i > 0 && steps <= blocks / 2)) continue;
-        const long held = strips < n ? strips : n, sms = room.sms.load(std::memory_order_relaxed);
-        const double share = (double)((held * blocks + sms - 1) / sms);
-        const double cost = (double)((strips + n - 1) / n) * (double)((steps + blocks - 1) / blocks) * (share < 1.6 ? 1.6 : share);
-        if (i == 0 || cost < least) best = blocks, least = cost;
+    for (int b = 1; b <= kCluster; ++b) {
+        const long n = room.clusters[b].load(std::memory_order_relaxed), sms = room.sms.load(std::memory_order_relaxed);
+        if (n == 0 || (b > 1 && b > steps)) continue;
+        const long held = strips < n ? strips : n;
+        const double share = (double)((held * b + sms - 1) / sms);
+        const double cost = (double)((strips + n - 1) / n) * (double)((steps + b - 1) / b) * (share < 2 ? 2 : share);
+        if (b == 1 || cost < least) best = b, least = cost;
     }
     return best;
 }
 
-template <typename Kernel, typename... Args>
-cudaError_t launch_clusters(Kernel kernel, int (*smem)(int), Room* rooms, const ScanArgs& a, cudaStream_t stream,
-                            Args... args) {
+template <typename T>
+bool map_tokens(CUtensorMap* map, const void* ptr, const ScanArgs& a, const Geo& G) {
+    auto fn = tma_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.T, (cuuint64_t)a.Z};
+    cuuint64_t strides[2] = {(cuuint64_t)a.d * sizeof(T), (cuuint64_t)a.T * a.d * sizeof(T)};
+    cuuint32_t box[3] = {(cuuint32_t)G.box, (cuuint32_t)G.tokens, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+              const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Tin, bool kShared, typename Kernel>
+cudaError_t launch_clusters(Kernel kernel, int (*smem)(int), Room* rooms, const ScanArgs& a, const Geo& G,
+                            cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64) return cudaErrorInvalidDevice;
     Room& room = rooms[dev];
     if (room.sms.load(std::memory_order_acquire) == 0 && (e = find_room(kernel, smem, &room)) != cudaSuccess) return e;
-    const long strips = Strips(a.Z, a.d).count, steps = scan_steps(a.T);
-    const int blocks = pick_blocks(room, strips, steps);
+    Maps maps{};
+    if (G.per_head > 1 &&
+        (!map_tokens<Tin>(&maps.x, a.x, a, G) || (!kShared && !map_tokens<float>(&maps.g, a.g, a, G)) ||
+         (a.dO && !map_tokens<Tin>(&maps.dO, a.dO, a, G))))
+        return cudaErrorInvalidValue;
+    const int blocks = pick_blocks(room, G.strips, G.steps);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    config(kernel, blocks, smem(blocks), strips, stream, &cfg, attr);
-    return cudaLaunchKernelEx(&cfg, kernel, a, args..., blocks, (int)steps);
+    config(kernel, blocks, smem(blocks), G.strips, stream, &cfg, attr);
+    return cudaLaunchKernelEx(&cfg, kernel, a, maps, G, blocks);
 }
 
 template <typename Tin, bool kShared>
 cudaError_t launch_fwd(const ScanArgs& a, cudaStream_t stream) {
     static Room rooms[64];
-    return launch_clusters(scan_fwd_kernel<Tin, kShared>, FwdSmem<Tin, kShared>::bytes, rooms, a, stream);
+    return launch_clusters<Tin, kShared>(scan_fwd_kernel<Tin, kShared>, FwdSmem<Tin, kShared>::bytes, rooms, a,
+                                         scan_geo(a.Z, a.T, a.d), stream);
 }
 
 template <typename Tin, bool kShared>
 cudaError_t launch_bwd(const ScanArgs& a, cudaStream_t stream) {
     static Room rooms[64];
-    const int per_head = Strips(a.Z, a.d).per_head;
-    float* parts = static_cast<float*>(a.scratch);
-    const cudaError_t e = launch_clusters(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::bytes, rooms, a, stream,
-                                          (const float*)a.E, parts);
-    if (e != cudaSuccess || !kShared || per_head == 1) return e;
+    const Geo G = scan_geo(a.Z, a.T, a.d);
+    const cudaError_t e =
+        launch_clusters<Tin, kShared>(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::bytes, rooms, a, G, stream);
+    if (e != cudaSuccess || !kShared || G.per_head == 1) return e;
     const long n = a.Z * a.T, blocks = (n + 255) / 256;
-    scan_parts_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(parts, a.dg, n, per_head);
+    scan_parts_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(static_cast<const float*>(a.scratch),
+                                                                                    a.dg, n, G.per_head);
     return cudaGetLastError();
 }
 

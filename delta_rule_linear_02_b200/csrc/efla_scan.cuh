@@ -82,7 +82,6 @@ __device__ __forceinline__ void scan_gates2(int rule, float2 g, float2* a, float
 
 // Streams [Z][T][d] (dense: Z = B*H, one sequence each; packed: Z = H, sequences cu[n] ..
 // cu[n+1] of every stream); states [(n * Z + z) * d], n = 0 for dense batches.
-constexpr int kScanChunk = 32;      // tokens between two saved states
 struct ScanArgs {
     const void* x = nullptr;
     const float* g = nullptr;       // [Z][T][gw], gw = d or 1
@@ -93,7 +92,7 @@ struct ScanArgs {
     const float* S0 = nullptr;
     void* o = nullptr;              // forward; null: states only
     float* S_T = nullptr;
-    float* E = nullptr;             // the state before token 64 c, by strips (written by the forward)
+    float* E = nullptr;             // the state entering each tile, as efla_scan.cu lays them out (kept by the forward)
     // backward
     const void* dO = nullptr;
     const float* dST = nullptr;
