@@ -94,37 +94,36 @@ __device__ __forceinline__ Lane lane_of(const Geo& G, long Z, int d, int strip, 
 // contiguous per head (one bulk copy each, about a tenth faster than TMA boxes); what lies behind
 // the end or beside the last head is zeroed.  A part of a wide head is a TMA box, which fills
 // with zeros itself.
-struct Tile {
-    int t0, rows, heads;      // tokens and heads that there are
-};
-__device__ __forceinline__ Tile tile_at(const Geo& G, long Z, int T, int strip, int chunk) {
-    Tile t;
-    t.t0 = chunk * G.tokens;
-    t.rows = min(G.tokens, T - t.t0);
-    t.heads = (int)min((long)G.heads, Z - (long)(strip / G.per_head) * G.heads);
-    return t;
-}
-__device__ __forceinline__ int tile_values(const Geo& G, const Tile& t) {
-    return G.per_head > 1 ? G.tokens * G.box : t.heads * t.rows * G.box;
-}
-template <typename T>
-__device__ __forceinline__ void zero_rest(T* dst, const Geo& G, const Tile& t) {
-    if (G.per_head > 1 || (t.rows == G.tokens && t.heads == G.heads)) return;
-    const int lane = threadIdx.x & 31, head = G.tokens * G.box, there = t.rows * G.box;
-    for (int p = 0; p < G.heads; ++p)
-        for (int i = (p < t.heads ? there : 0) + lane * 4; i < head; i += 128) st4(dst + p * head + i, all4(0.f));
-}
-template <typename T>
-__device__ __forceinline__ void stage(T* dst, const T* src, const CUtensorMap* map, const Geo& G, int Ttot, int strip,
-                                      const Tile& t, uint64_t* bar) {
-    const int lane = threadIdx.x & 31;
-    if (G.per_head > 1) {
-        if (lane == 0) tma_load_3d(dst, map, bar, (strip % G.per_head) * G.width, t.t0, strip / G.per_head);
-    } else if (lane < t.heads) {
-        const long z = (long)strip * G.heads + lane;
-        bulk_load(dst + lane * G.tokens * G.box, src + (z * Ttot + t.t0) * G.box, t.rows * G.box * (int)sizeof(T), bar);
+struct Stager {
+    int heads, z0, c0;        // heads that there are, the first of them, and the first channel
+    const Geo& G;
+    long T;
+    __device__ __forceinline__ Stager(const Geo& G_, long Z, int T_, int strip) : G(G_), T(T_) {
+        z0 = G.per_head > 1 ? strip / G.per_head : strip * G.heads;
+        c0 = G.per_head > 1 ? (strip % G.per_head) * G.width : 0;
+        heads = (int)min((long)G.heads, Z - z0);
     }
-}
+    __device__ __forceinline__ int rows(int t0) const { return (int)min((long)G.tokens, T - t0); }
+    __device__ __forceinline__ int values(int t0) const {
+        return G.per_head > 1 ? kValues : heads * rows(t0) * G.box;
+    }
+    template <typename E>
+    __device__ __forceinline__ void zero_rest(E* dst, int t0) const {
+        if (G.per_head > 1 || (T - t0 >= G.tokens && heads == G.heads)) return;
+        const int lane = threadIdx.x & 31, head = G.tokens * G.box, there = rows(t0) * G.box;
+        for (int p = 0; p < G.heads; ++p)
+            for (int i = (p < heads ? there : 0) + lane * 4; i < head; i += 128) st4(dst + p * head + i, all4(0.f));
+    }
+    template <typename E>
+    __device__ __forceinline__ void stage(E* dst, const E* src, const CUtensorMap* map, int t0, uint64_t* bar) const {
+        const int lane = threadIdx.x & 31;
+        if (G.per_head > 1) {
+            if (lane == 0) tma_load_3d(dst, map, bar, c0, t0, z0);
+        } else if (lane < heads) {
+            bulk_load(dst + lane * G.tokens * G.box, src + ((z0 + lane) * T + t0) * G.box, rows(t0) * G.box * (int)sizeof(E), bar);
+        }
+    }
+};
 
 // The packed sequence that holds token t: the largest n with cu[n] <= t.
 __device__ __forceinline__ int seq_of(const ScanArgs& P, int t) {
@@ -149,6 +148,10 @@ struct MarkRing {
 __device__ __forceinline__ void make_marks(const ScanArgs& P, const Geo& G, int chunk, MarkRing* ring, int slot) {
     const int lane = threadIdx.x & 31;
     uint32_t any = 0;
+    if (!P.cu && chunk > 0 && P.T - chunk * G.tokens > G.tokens) {
+        if (lane == 0) ring->any[slot] = 0;
+        return;
+    }
     for (int j = 0; j < G.groups; ++j) {
         const int t = chunk * G.tokens + 32 * j + lane, n = t < P.T ? seq_of(P, t) : 0;
         const uint32_t first = __ballot_sync(0xffffffffu, t < P.T && (P.cu ? P.cu[n] == t : t == 0));
@@ -345,21 +348,22 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         fence_mbar_init();
     }
     __syncthreads();
+    const Stager stager(G, P.Z, P.T, strip);
     auto prefetch = [&](int n) {      // by the last warp
         const int chunk = n * blocks + rank;
         if (chunk >= G.steps) return;
         const int st = n % M::kStages;
-        const Tile t = tile_at(G, P.Z, P.T, strip, chunk);
+        const int t0 = chunk * G.tokens;
         Tin* dx = reinterpret_cast<Tin*>(smem + st * M::kStage);
         float* dg = reinterpret_cast<float*>(smem + st * M::kStage + M::kX);
         make_marks(P, G, chunk, ring, n % kMarks);
-        zero_rest(dx, G, t);
-        if (!kShared) zero_rest(dg, G, t);
+        stager.zero_rest(dx, t0);
+        if (!kShared) stager.zero_rest(dg, t0);
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full + st, tile_values(G, t) * (int)(sizeof(Tin) + (kShared ? 0 : 4)));
+        if (lane == 0) mbar_arrive_expect_tx(full + st, stager.values(t0) * (int)(sizeof(Tin) + (kShared ? 0 : 4)));
         __syncwarp();
-        stage(dx, static_cast<const Tin*>(P.x), &maps.x, G, P.T, strip, t, full + st);
-        if (!kShared) stage(dg, P.g, &maps.g, G, P.T, strip, t, full + st);
+        stager.stage(dx, static_cast<const Tin*>(P.x), &maps.x, t0, full + st);
+        if (!kShared) stager.stage(dg, P.g, &maps.g, t0, full + st);
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
@@ -380,13 +384,13 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                 wait_or_give_up(ready, n & 1, &dead, P.err);
                 f = fold_runs<false>(runA, runB, G.width);
             }
-            if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);      // the stage has been read
             const float2 h = chain_turn(f, blocks, G, rank * G.groups + part, pair, n, sent, got, &carry, &dead, P.err);
             if (tile) {
                 enter_runs<false>(runA, runB, G.width, h);
                 warp_arrive(entered);
                 if (P.E && part == 0)
                     *reinterpret_cast<float2*>(P.E + ((size_t)chunk * G.strips + strip) * G.width + pair * 2) = h;
+                if (warp == kThreads / 32 - 1) prefetch(n + M::kStages);      // the stage was read before `ready`
             }
         }
     } else {
@@ -394,6 +398,13 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         float* run = runs + warp * kLanes4 + lane * 4;
         const Tin* x0 = reinterpret_cast<const Tin*>(smem) + L.smem;
         const float* g0 = reinterpret_cast<const float*>(smem + M::kX) + L.smem;
+        float gn[kRun];                    // a shared decay's values for the next turn
+        auto load_shared = [&](int n) {
+            const int t = (n * blocks + rank) * G.tokens + L.run * kRun;
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) gn[i] = L.on && t + i < P.T ? P.g[L.z * P.T + t + i] : 0.f;
+        };
+        if (kShared) load_shared(0);
         for (int n = 0; n < turns; ++n) {
             const int chunk = n * blocks + rank;
             if (chunk >= G.steps) break;
@@ -402,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
             float gs[kRun];
             if (kShared) {
 #pragma unroll
-                for (int i = 0; i < kRun; ++i) gs[i] = i < live ? P.g[L.z * P.T + tw + i] : 0.f;
+                for (int i = 0; i < kRun; ++i) gs[i] = gn[i];
+                load_shared(n + 1);
             }
             wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
             const Tin* xs = x0 + st * (M::kStage / (int)sizeof(Tin));
@@ -423,11 +435,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                     if (!plain && (first >> i & 1u)) {       // a sequence begins: its own state enters, no other
                         if (P.S0 && L.on)
                             b[i] = fma4(a1, ld4(P.S0 + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c), b[i]);
-                        a1 = rb = all4(0.f);
+                        a1 = all4(0.f);
                     }
                     a.set(i, a1);
-                    ra = mul4(ra, a1);
-                    rb = fma4(a1, rb, b[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    if (!plain && (first >> i & 1u)) rb = all4(0.f);
+                    ra = mul4(ra, a.at(i));
+                    rb = fma4(a.at(i), rb, b[i]);
                 }
                 if (!plain && first) ra = all4(kCut);
                 st4(run, ra);
@@ -497,23 +513,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
         fence_mbar_init();
     }
     __syncthreads();
+    const Stager stager(G, P.Z, P.T, strip);
     auto prefetch = [&](int n) {
         const int chunk = G.steps - 1 - (n * blocks + rank);
         if (chunk < 0) return;
         const int st = n % M::kStages;
-        const Tile t = tile_at(G, P.Z, P.T, strip, chunk);
+        const int t0 = chunk * G.tokens;
         Tin* sx = reinterpret_cast<Tin*>(smem + st * M::kStage);
         float* sg = reinterpret_cast<float*>(smem + st * M::kStage + 2 * M::kX);
         make_marks(P, G, chunk, ring, n % kMarks);
-        zero_rest(sx, G, t);
-        zero_rest(sx + kValues, G, t);
-        if (!kShared) zero_rest(sg, G, t);
+        stager.zero_rest(sx, t0);
+        stager.zero_rest(sx + kValues, t0);
+        if (!kShared) stager.zero_rest(sg, t0);
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full + st, tile_values(G, t) * (int)(2 * sizeof(Tin) + (kShared ? 0 : 4)));
+        if (lane == 0) mbar_arrive_expect_tx(full + st, stager.values(t0) * (int)(2 * sizeof(Tin) + (kShared ? 0 : 4)));
         __syncwarp();
-        stage(sx, static_cast<const Tin*>(P.x), &maps.x, G, P.T, strip, t, full + st);
-        stage(sx + kValues, static_cast<const Tin*>(P.dO), &maps.dO, G, P.T, strip, t, full + st);
-        if (!kShared) stage(sg, P.g, &maps.g, G, P.T, strip, t, full + st);
+        stager.stage(sx, static_cast<const Tin*>(P.x), &maps.x, t0, full + st);
+        stager.stage(sx + kValues, static_cast<const Tin*>(P.dO), &maps.dO, t0, full + st);
+        if (!kShared) stager.stage(sg, P.g, &maps.g, t0, full + st);
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
@@ -565,6 +582,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
         const Tin* x0 = reinterpret_cast<const Tin*>(smem) + L.smem;
         const float* g0 = reinterpret_cast<const float*>(smem + 2 * M::kX) + L.smem;
         float* parts = static_cast<float*>(P.scratch);
+        float gn[kRun];                    // a shared decay's values for the next turn
+        auto load_shared = [&](int n) {
+            const int t = (G.steps - 1 - (n * blocks + rank)) * G.tokens + L.run * kRun;
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) gn[i] = L.on && t >= 0 && t + i < P.T ? P.g[L.z * P.T + t + i] : 0.f;
+        };
+        if (kShared) load_shared(0);
         for (int n = 0; n < turns; ++n) {
             const int chunk = G.steps - 1 - (n * blocks + rank);
             if (chunk < 0) break;
@@ -573,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
             float gs[kRun];
             if (kShared) {
 #pragma unroll
-                for (int i = 0; i < kRun; ++i) gs[i] = i < live ? P.g[L.z * P.T + tw + i] : 0.f;
+                for (int i = 0; i < kRun; ++i) gs[i] = gn[i];
+                load_shared(n + 1);
             }
             wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
             const Tin* xs = x0 + st * (M::kStage / (int)sizeof(Tin));
