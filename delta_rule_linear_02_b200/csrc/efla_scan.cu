@@ -721,12 +721,22 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Tin* __restrict__ 
 }
 
 // ---------------------------------------------------------------- host
-// The widest strips that still give every SM something to do (48 strips with clusters of up to
-// eight blocks), leave at most a quarter of the lanes without a channel, and a tile of which is
-// not longer than the sequence; or the best that can be had of these.
+// The time of a scan, in microseconds as measured on a B200 (tiles of 4096 bf16 values with a decay
+// per channel): a turn takes 1.3, 1.8 and 2.3 with one to three blocks on an SM, and the exchange
+// about 0.2 + 0.13 per block of the cluster; `held` clusters run at once, the others after them.
+double scan_cost(long strips, long steps, int groups, int blocks, long held, long sms) {
+    const long rounds = (strips + held - 1) / held, turns = (steps + blocks - 1) / blocks;
+    const long share = ((strips < held ? strips : held) * blocks + sms - 1) / sms;
+    const double exchange = blocks > 1 ? 0.2 + 0.13 * blocks : groups > 1 ? 0.1 : 0.0;
+    return (double)(rounds * turns) * (0.75 + 0.53 * (double)share + exchange);
+}
+
+// The strips' width: the one with the least time at its best number of blocks, on 148 SMs with
+// three blocks each.  (64 heads of 128, T 2048: 37.5 us at width 128 with four blocks, 34 at 32 with
+// one; 16 heads, T 32768: 263 us at 128 with eight, 133 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
 Geo scan_geo(long Z, int T, int d) {
     Geo best{};
-    double most = -1;
+    double least = 0;
     for (int groups = 1; groups <= 4; groups *= 2) {
         Geo G;
         G.groups = groups;
@@ -737,10 +747,12 @@ Geo scan_geo(long Z, int T, int d) {
         G.strips = (int)(G.heads > 1 ? (Z + G.heads - 1) / G.heads : Z * G.per_head);
         G.steps = (int)(((long)T + G.tokens - 1) / G.tokens);
         G.box = d < G.width ? d : G.width;
-        const double used = (double)Z * d / ((double)G.strips * G.width), fill = G.strips < 48 ? G.strips / 48.0 : 1.0;
-        if (groups > 1 && T <= G.tokens / 2) break;
-        if (used * fill > most + 1e-9) best = G, most = used * fill;
-        if (used >= 0.75 && fill >= 1.0) break;
+        double cost = 0;
+        for (int b = 1; b <= kCluster && (b == 1 || b <= G.steps); ++b) {
+            const double c = scan_cost(G.strips, G.steps, groups, b, 444 / b, 148);
+            if (b == 1 || c < cost) cost = c;
+        }
+        if (groups == 1 || cost < least) best = G, least = cost;
     }
     return best;
 }
@@ -809,19 +821,14 @@ cudaError_t find_room(Kernel kernel, int (*smem)(int), Room* room) {
     return cudaSuccess;
 }
 
-// Blocks per cluster: a strip takes ceil(steps / blocks) turns, in as many rounds as the device
-// needs to hold all strips' clusters; a turn takes as long as the blocks that share an SM need,
-// and with fewer than two of them its own latency.
-int pick_blocks(const Room& room, long strips, long steps) {
+int pick_blocks(const Room& room, const Geo& G) {
     int best = 1;
     double least = 0;
-    for (int b = 1; b <= kCluster; ++b) {
-        const long n = room.clusters[b].load(std::memory_order_relaxed), sms = room.sms.load(std::memory_order_relaxed);
-        if (n == 0 || (b > 1 && b > steps)) continue;
-        const long held = strips < n ? strips : n;
-        const double share = (double)((held * b + sms - 1) / sms);
-        const double cost = (double)((strips + n - 1) / n) * (double)((steps + b - 1) / b) * (share < 2 ? 2 : share);
-        if (b == 1 || cost < least) best = b, least = cost;
+    for (int b = 1; b <= kCluster && (b == 1 || b <= G.steps); ++b) {
+        const long held = room.clusters[b].load(std::memory_order_relaxed);
+        if (held == 0) continue;
+        const double c = scan_cost(G.strips, G.steps, G.groups, b, held, room.sms.load(std::memory_order_relaxed));
+        if (b == 1 || c < least) best = b, least = c;
     }
     return best;
 }
@@ -853,7 +860,7 @@ cudaError_t launch_clusters(Kernel kernel, int (*smem)(int), Room* rooms, const 
         (!map_tokens<Tin>(&maps.x, a.x, a, G) || (!kShared && !map_tokens<float>(&maps.g, a.g, a, G)) ||
          (a.dO && !map_tokens<Tin>(&maps.dO, a.dO, a, G))))
         return cudaErrorInvalidValue;
-    const int blocks = pick_blocks(room, G.strips, G.steps);
+    const int blocks = pick_blocks(room, G);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     config(kernel, blocks, smem(blocks), G.strips, stream, &cfg, attr);
