@@ -145,21 +145,28 @@ struct MarkRing {
     Marks m[kMarks];
     uint32_t any[kMarks];
 };
-__device__ __forceinline__ void make_marks(const ScanArgs& P, const Geo& G, int chunk, MarkRing* ring, int slot) {
+// One warp: the sequences from the one that holds t0 on, a lane each.  (A call, so that what few
+// tiles need costs the kernels no registers.)
+__device__ __noinline__ bool find_marks(const int* cu, int nseq, int n0, int T, int t0, int t1, Marks* m) {
     const int lane = threadIdx.x & 31;
-    uint32_t any = 0;
-    if (!P.cu && chunk > 0 && P.T - chunk * G.tokens > G.tokens) {
-        if (lane == 0) ring->any[slot] = 0;
-        return;
+    uint32_t* words = m->first;                // and m->last behind it
+    if (lane < 8) words[lane] = 0;
+    __syncwarp();
+    bool any = false;
+    for (;; n0 += 32) {
+        const int n = n0 + lane;
+        const int from = n >= nseq ? t1 : cu ? cu[n] : 0, to = n >= nseq ? t1 : cu ? cu[n + 1] : T;
+        if (from < to && from >= t0 && from < t1) atomicOr(words + ((from - t0) >> 5), 1u << ((from - t0) & 31)), any = true;
+        if (from < to && to > t0 && to <= t1) atomicOr(words + 4 + ((to - 1 - t0) >> 5), 1u << ((to - 1 - t0) & 31)), any = true;
+        if (__any_sync(0xffffffffu, from >= t1)) break;
     }
-    for (int j = 0; j < G.groups; ++j) {
-        const int t = chunk * G.tokens + 32 * j + lane, n = t < P.T ? seq_of(P, t) : 0;
-        const uint32_t first = __ballot_sync(0xffffffffu, t < P.T && (P.cu ? P.cu[n] == t : t == 0));
-        const uint32_t last = __ballot_sync(0xffffffffu, t < P.T && (P.cu ? P.cu[n + 1] : P.T) == t + 1);
-        if (lane == 0) ring->m[slot].first[j] = first, ring->m[slot].last[j] = last;
-        any |= first | last;
-    }
-    if (lane == 0) ring->any[slot] = any;
+    return __any_sync(0xffffffffu, any);
+}
+__device__ __forceinline__ void make_marks(const ScanArgs& P, const Geo& G, int chunk, MarkRing* ring, int slot) {
+    const int t0 = chunk * G.tokens, left = P.T - t0;
+    const bool any = (P.cu || t0 == 0 || left <= G.tokens) &&
+                     find_marks(P.cu, P.cu ? P.nseq : 1, seq_of(P, t0), P.T, t0, t0 + min(G.tokens, left), ring->m + slot);
+    if ((threadIdx.x & 31) == 0) ring->any[slot] = any;
 }
 __device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
     return words[run >> 3] >> (run & 7) * kRun & ((1u << kRun) - 1u);
@@ -306,6 +313,30 @@ __device__ __forceinline__ void token_gates(int rule, const float* gt, float gs,
         const P4 g = ld4(gt);
         scan_gates2<kSlope>(rule, g.lo, &a->lo, &w->lo, &dw->lo);
         scan_gates2<kSlope>(rule, g.hi, &a->hi, &w->hi, &dw->hi);
+    }
+}
+
+// The sums of four tokens over `span` lanes, stored to to[0 .. live).  In the first two steps a lane
+// passes on the tokens that it does not keep, so one value is left for the others: six shuffles
+// instead of twenty.
+__device__ __forceinline__ void sum_tokens(const float* sum, float* to, int span, int lane, int live) {
+    if (span >= 4) {
+        const bool b0 = lane & 1, b1 = lane & 2;
+        float t0 = (b0 ? sum[2] : sum[0]) + __shfl_xor_sync(0xffffffffu, b0 ? sum[0] : sum[2], 1);
+        float t1 = (b0 ? sum[3] : sum[1]) + __shfl_xor_sync(0xffffffffu, b0 ? sum[1] : sum[3], 1);
+        float u = (b1 ? t1 : t0) + __shfl_xor_sync(0xffffffffu, b1 ? t0 : t1, 2);
+#pragma unroll
+        for (int far = 4; far <= 16; far *= 2)
+            if (far < span) u += __shfl_xor_sync(0xffffffffu, u, far);
+        const int i = 2 * b0 + b1;
+        if (lane % span < 4 && i < live) to[i] = u;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        float u = sum[i];
+        if (span == 2) u += __shfl_xor_sync(0xffffffffu, u, 1);
+        if (lane % span == 0 && i < live) to[i] = u;
     }
 }
 
@@ -582,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
         const Tin* x0 = reinterpret_cast<const Tin*>(smem) + L.smem;
         const float* g0 = reinterpret_cast<const float*>(smem + 2 * M::kX) + L.smem;
         float* parts = static_cast<float*>(P.scratch);
+        const int span = G.heads > 1 ? P.d / 4 : G.width / 4;      // lanes of a head
         float gn[kRun];                    // a shared decay's values for the next turn
         auto load_shared = [&](int n) {
             const int t = (G.steps - 1 - (n * blocks + rank)) * G.tokens + L.run * kRun;
@@ -653,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
                 }
                 // 3. the gradients
                 P4 c = ld4(run + 3 * M::kRuns);
+                float sum[kRun];
                 float* dx = P.dx + (L.z * P.T + tw) * P.d + L.c;
                 float* dg = P.dg + (L.z * P.T + tw) * (kShared ? 1 : P.d) + (kShared ? 0 : L.c);
 #pragma unroll
@@ -665,16 +698,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
                         st4(dx + i * P.d, mul4(w.at(i), Gt));
                         if (!kShared) st4(dg + i * P.d, dgv);
                     }
-                    if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
-                        float sum = i < live ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
-                        const int span = G.heads > 1 ? P.d / 4 : G.width / 4;
-                        for (int far = span / 2; far > 0; far >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, far);
-                        if (i < live && lane % span == 0) {
-                            if (G.per_head == 1) dg[i] = sum;
-                            else parts[((long)(strip % G.per_head) * P.Z + L.z) * P.T + tw + i] = sum;
-                        }
-                    }
+                    if (kShared) sum[i] = L.on ? (dgv.lo.x + dgv.lo.y) + (dgv.hi.x + dgv.hi.y) : 0.f;
                     if (!plain && P.dS0 && (first >> i & 1u) && L.on) st4(P.dS0 + row_of(i), c);
+                }
+                if (kShared) {      // over the head's channels; a part of a wide head leaves a partial sum
+                    float* to = G.per_head == 1 ? dg : parts + ((long)(strip % G.per_head) * P.Z + L.z) * P.T + tw;
+                    sum_tokens(sum, to, span, lane, L.z < P.Z ? P.T - tw : 0);
                 }
             };
             if (ring->any[n % kMarks]) tile(std::false_type(), std::integral_constant<int, -1>());
