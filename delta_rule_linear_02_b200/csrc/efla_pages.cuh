@@ -50,6 +50,19 @@ struct RowPages {
     bool active;
     long write, read;      // pages; read < 0: from a zero state
 };
+__device__ __forceinline__ RowPages row_pages(const PagedRows& P, int slot, int src, bool* bad) {
+    RowPages r{true, -1, -1};
+    if (slot < 0 || slot >= P.n_slots) *bad = true;
+    else r.write = P.table[slot];
+    if (src == slot) r.read = r.write;
+    else if (src != -1) {
+        if (src < 0 || src >= P.n_slots) *bad = true;
+        else r.read = P.table[src];
+        *bad |= r.read < 0 || r.read >= P.n_pages;
+    }
+    *bad |= r.write < 0 || r.write >= P.n_pages;
+    return r;
+}
 __device__ __forceinline__ RowPages paged_row(const PagedRows& P, int N, int n) {
     const int slot = P.slots[n];
     if (slot == -1) return RowPages{false, -1, -1};
@@ -58,16 +71,7 @@ __device__ __forceinline__ RowPages paged_row(const PagedRows& P, int N, int n) 
     for (int m = threadIdx.x; m < n; m += blockDim.x) bad |= P.slots[m] == slot;
     if (src != slot && src != -1)
         for (int m = threadIdx.x; m < N; m += blockDim.x) bad |= P.slots[m] == src;
-    RowPages r{true, -1, -1};
-    if (slot < 0 || slot >= P.n_slots) bad = true;
-    else r.write = P.table[slot];
-    if (src == slot) r.read = r.write;
-    else if (src != -1) {
-        if (src < 0 || src >= P.n_slots) bad = true;
-        else r.read = P.table[src];
-        bad |= r.read < 0 || r.read >= P.n_pages;
-    }
-    bad |= r.write < 0 || r.write >= P.n_pages;
+    RowPages r = row_pages(P, slot, src, &bad);
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) atomicOr(P.err, kPagesBadSlot);
         r.active = false;

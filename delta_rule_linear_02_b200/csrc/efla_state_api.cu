@@ -394,6 +394,7 @@ int efla_pages_status(void* pages, int clear, efla_stream_t stream) {
     if (cudaStreamSynchronize(s) != cudaSuccess) return EFLA_ERR_CUDA;
     if (clear && (cudaMemsetAsync(pages, 0, sizeof(word), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
         return EFLA_ERR_CUDA;
+    if (word & efla::kDevTimeout) return EFLA_ERR_TIMEOUT;
     if (word & efla::kPagesBadSlot) return EFLA_ERR_SLOT;
     return word & efla::kPagesFull ? EFLA_ERR_FULL : EFLA_OK;
 }

@@ -194,7 +194,7 @@ def pages_of(ref, slots, source=None):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["delta", "gated", "scan", "scan shared"])
-@pytest.mark.parametrize("N,H,d", [(1, 1, 64), (7, 3, 64), (5, 16, 128), (40, 2, 128)])
+@pytest.mark.parametrize("N,H,d", [(1, 1, 64), (7, 3, 64), (5, 16, 128), (40, 2, 128), (150, 3, 128), (333, 3, 64), (160, 7, 64)])
 @pytest.mark.parametrize("rule", [EXACT, EULER])
 def test_paged_steps(efla, cuda, N, H, d, kind, dtype, rule):
     shape = (H, d, d) if kind in ("delta", "gated") else (H, d)
