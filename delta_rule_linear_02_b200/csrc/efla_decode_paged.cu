@@ -135,6 +135,10 @@ struct StreamSmem {
     static constexpr int kBytes = kRing * kJobFloats * 4 + kRing * 3 * kRow + 4 * kRed + kRing * (int)sizeof(Job) + 8 * 8;
 };
 
+// All but the last N of the thread's bulk stores have read their source.
+template <int N>
+__device__ __forceinline__ void wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+
 // A row's pages as paged_row gives them, by one warp.
 __device__ __forceinline__ RowPages paged_row_warp(const PagedRows& P, int N, int n) {
     const int lane = threadIdx.x & 31, slot = P.slots[n];
@@ -180,12 +184,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1) decode_stream_kernel(const 
         RowPages pg{false, -1, -1};
         int row = -1, sent = 0;
         bool ok = true;
-        auto write_back = [&](int j) {    // job j is done: its state leaves the buffer
+        // Job j is done: its state leaves the buffer in quarters, and as soon as a quarter has been read
+        // the next job's may take its place (`load(quarter)`).
+        auto write_back = [&](int j, auto load) {
             const int b = j % kRing;
             ok = ok && __all_sync(0xffffffffu, mbar_wait(done + b, j / kRing & 1, kWaitNs));
             if (ok && lane == 0) {
-                bulk_store(reinterpret_cast<float*>(pool) + jobs[b].out, ring + b * kJobFloats, jobs[b].heads * D * D * 4);
-                tma_store_wait_read();
+                const int quarter = jobs[b].heads * D * D / 4;
+                float* to = reinterpret_cast<float*>(pool) + jobs[b].out;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    bulk_store(to + i * quarter, ring + b * kJobFloats + i * quarter, quarter * 4);
+                load(b);
             }
             __syncwarp();
         };
@@ -196,28 +206,50 @@ __global__ void __launch_bounds__(kStreamThreads, 1) decode_stream_kernel(const 
                 row = n;
             }
             if (!pg.active) continue;
-            const int b = sent % kRing;
-            if (sent >= kRing) write_back(sent - kRing);
-            if (ok && lane == 0) {
+            const int b = sent % kRing, bytes = heads * D * (int)sizeof(Tin), quarter = heads * D * D;      // in bytes
+            const long at = ((long)n * H + h0) * D;
+            const char* from = pool + (pg.read < 0 ? 0 : pg.read) * (long)P.page_bytes + (long)h0 * D * D * 4;
+            char* to = reinterpret_cast<char*>(ring + b * kJobFloats);
+            auto begin = [&]() {
                 jobs[b] = Job{n, h0, heads, pg.read < 0, pg.write * (long)(P.page_bytes / 4) + (long)h0 * D * D};
-                const int bytes = heads * D * (int)sizeof(Tin);
-                mbar_arrive_expect_tx(full + b, 3 * bytes + (pg.read < 0 ? 0 : heads * D * D * 4));
-                if (pg.read >= 0)
-                    bulk_load(ring + b * kJobFloats, pool + pg.read * (long)P.page_bytes + (long)h0 * D * D * 4,
-                              heads * D * D * 4, full + b);
-                const long at = ((long)n * H + h0) * D;
+                mbar_arrive_expect_tx(full + b, 3 * bytes + (pg.read < 0 ? 0 : 4 * quarter));
                 bulk_load(rows + (b * 3 + 0) * M::kRow, q + at, bytes, full + b);
                 bulk_load(rows + (b * 3 + 1) * M::kRow, k + at, bytes, full + b);
                 bulk_load(rows + (b * 3 + 2) * M::kRow, v + at, bytes, full + b);
+            };
+            auto load = [&](int i) {
+                if (pg.read >= 0) bulk_load(to + i * quarter, from + i * quarter, quarter, full + b);
+            };
+            if (sent < kRing) {
+                if (lane == 0) {
+                    begin();
+                    for (int i = 0; i < 4; ++i) load(i);
+                }
+                __syncwarp();
+            } else {
+                // (a last job of fewer heads is shorter: then its quarters are not where the next one's go)
+                const bool same = jobs[b].heads == heads;
+                write_back(sent - kRing, [&](int) {
+                    begin();
+                    if (!same) wait_read<0>();
+                    wait_read<3>();
+                    load(0);
+                    wait_read<2>();
+                    load(1);
+                    wait_read<1>();
+                    load(2);
+                    wait_read<0>();
+                    load(3);
+                });
             }
             ++sent;
         }
-        if (sent >= kRing) write_back(sent - kRing);
+        if (sent >= kRing) write_back(sent - kRing, [](int) {});
         if (ok && lane == 0) {            // the end, in the next buffer
             jobs[sent % kRing].n = -1;
             mbar_arrive(full + sent % kRing);
         }
-        for (int j = max(0, sent - kRing + 1); j < sent; ++j) write_back(j);
+        for (int j = max(0, sent - kRing + 1); j < sent; ++j) write_back(j, [](int) {});
         if (!ok && lane == 0) atomicOr(P.err, kDevTimeout);
         tma_store_wait_all();
         return;

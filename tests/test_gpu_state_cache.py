@@ -235,10 +235,11 @@ def test_paged_steps(efla, cuda, N, H, d, kind, dtype, rule):
                 assert torch.equal(o[n], marker[n])
 
 
+@pytest.mark.parametrize("H", [2, 150])
 @pytest.mark.parametrize("kind", ["delta", "scan"])
-def test_paged_steps_refuse_rows(efla, cuda, kind):
+def test_paged_steps_refuse_rows(efla, cuda, kind, H):
     """Rows that would be wrong or race are left out whole; the others are what they would be alone."""
-    N, H, d = 9, 2, 64
+    N, d = 9, 64
     shape = (H, d, d) if kind == "delta" else (H, d)
     b = filled(efla, 14, 12, 10, shape)
     c = {n: t.cuda() for n, t in step_case(N, H, d, torch.float32, 1).items()}
