@@ -7,7 +7,6 @@ it has not been built (python delta_rule_linear_02_b200/build.py).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -499,9 +498,18 @@ def efla_backward(q, k, v, beta, dO, S0=None, dS_T=None, want_dS0: bool = True, 
 # ---------------------------------------------------------------- the per-channel gated recurrence
 def _call(fn, where: str, device: torch.device, stream, *args):
     """fn(*args, stream) with the tensors' device current; `stream` None: that device's current one."""
-    with torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext():
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        status = fn(*args, s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
+    index = device.index
+    if index is None:
+        raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)      # torch.cuda.current_stream costs 2 us of every call
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
     if status != EFLA_OK:
         raise EflaError(status, where)
 
@@ -510,15 +518,15 @@ def _tensor(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optio
     """The address of a contiguous tensor of this type, device and shape (None: NULL)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+        raise ValueError(f"{name} must be on {device if device.type == 'cuda' else 'a CUDA device'}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _scan_shape(x: torch.Tensor, g: torch.Tensor, cu_seqlens):
@@ -683,15 +691,18 @@ def _pool(pool: torch.Tensor, pages: EflaPages, dtype=None) -> Tuple[int, int, i
         raise ValueError(f"pool must be on {pages.block.device}, got {pool.device}")
     if dtype is not None and pool.dtype != dtype:
         raise ValueError(f"pool must be {dtype}, got {pool.dtype}")
-    if pool.dim() < 2 or pool.shape[0] != pages.n_pages or not pool[0].is_contiguous():
-        raise ValueError(f"pool must be [{pages.n_pages}, ...] with contiguous pages, got {tuple(pool.shape)}")
-    es = pool.element_size()
-    data = pool[0].numel() * es
-    return pool.data_ptr(), (pool.stride(0) * es if pages.n_pages > 1 else data), data
+    n, es = pages.n_pages, pool.element_size()
+    if pool.dim() >= 2 and pool.shape[0] == n:
+        data = pool.numel() // n * es
+        if pool.is_contiguous():
+            return pool.data_ptr(), data, data
+        if pool[0].is_contiguous():
+            return pool.data_ptr(), pool.stride(0) * es if n > 1 else data, data
+    raise ValueError(f"pool must be [{n}, ...] with contiguous pages, got {tuple(pool.shape)}")
 
 
 def _slots(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None) -> Optional[int]:
-    return _tensor(t, name, torch.int32, device, (t.numel() if n is None else n,)) if t is not None else None
+    return None if t is None else _tensor(t, name, torch.int32, device, (t.numel() if n is None else n,))
 
 
 def efla_pages_fork(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Tensor, stream=None) -> None:

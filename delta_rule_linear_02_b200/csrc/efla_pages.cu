@@ -1,8 +1,13 @@
 // efla_pages.cu -- pages of the state cache: init, free, fork, copy, compact, rows in and out.
 //
-// A page holds the whole recurrent state of one sequence; a slot names a sequence.  Plans (which
-// page goes where) are made by one block from the lists alone, so they are the same on every
-// run; the data then moves with every byte read once and written once.
+// A page holds the whole recurrent state of one sequence; a slot names a sequence.  A plan (which
+// page goes where) follows from the lists, the table and the owners alone, so it is the same on
+// every run; the data then moves with every byte read once and written once.
+//
+// For caches of up to 4096 pages and lists of up to 256 entries one launch does both: every block
+// makes the whole plan for itself in shared memory (about 2 us, instead of a second launch and
+// its wait, about 5), moves its share, and the last one to finish writes the new table and owners,
+// which the others have by then read.  Larger ones take a launch of one block for the plan.
 #include "efla_kernels.h"
 #include "efla_pages.cuh"
 
@@ -185,37 +190,200 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan(PagesBlock b)
     if (threadIdx.x == 0) *b.moves = late;
 }
 
-// The planned moves, where no page is both read and written.
-__global__ void __launch_bounds__(256) pages_move_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs) {
-    const long total = (long)*b.moves * vecs;
-    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
-        const int m = (int)(i / vecs);
-        const size_t at = (size_t)(i % vecs) * 16;
-        const int from = b.src[m];
-        const uint4 v = from < 0 ? make_uint4(0, 0, 0, 0)
-                                 : *reinterpret_cast<const uint4*>(pool + (size_t)from * page_bytes + at);
-        *reinterpret_cast<uint4*>(pool + (size_t)b.dst[m] * page_bytes + at) = v;
+// ---------------------------------------------------------------- moves
+constexpr int kMoveThreads = 256, kUnit = 4 * kMoveThreads;      // 16-byte vectors of a block's piece: 16 KiB
+
+// The block's share of the moves src[m] -> dst[m] (src < 0: zeros), where no page is both.
+__device__ __forceinline__ void move_pages(const int* src, const int* dst, int moves, char* pool, size_t page_bytes,
+                                           long vecs) {
+    const long pieces = (vecs + kUnit - 1) / kUnit, total = moves * pieces;
+    for (long u = blockIdx.x; u < total; u += gridDim.x) {
+        const int m = (int)(u / pieces);
+        const long v0 = (u % pieces) * kUnit + threadIdx.x;
+        const int from = src[m];
+        const uint4* in = reinterpret_cast<const uint4*>(pool + (size_t)(from < 0 ? 0 : from) * page_bytes);
+        uint4* out = reinterpret_cast<uint4*>(pool + (size_t)dst[m] * page_bytes);
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (from >= 0 && v0 + i * kMoveThreads < vecs) v[i] = __ldcs(in + v0 + i * kMoveThreads);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (v0 + i * kMoveThreads < vecs) __stcs(out + v0 + i * kMoveThreads, v[i]);
     }
 }
 
-// The planned moves as if all at once: a block owns a strip of `width` 16-byte columns of every
-// page, reads it for all moves into shared memory, then writes it.
-__global__ void __launch_bounds__(256) pages_strip_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs,
-                                                          int width) {
-    extern __shared__ uint4 held[];
+__global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs) {
+    move_pages(b.src, b.dst, *b.moves, pool, page_bytes, vecs);
+}
+
+// Exclusive prefix sum over the block's threads; *total: the block's sum.
+__device__ __forceinline__ int block_sum(int value, int* total) {
+    __shared__ int warps[kMoveThreads / 32 + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = value;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += up;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = sum;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kMoveThreads / 32; ++w) {
+        if (w == warp) before = all;
+        all += warps[w];
+    }
+    *total = all;
+    return before + sum - value;
+}
+
+// Whether entry i (source `from`, destination `to`) may run: as plan_entry, with the list in
+// shared memory instead of claims.
+__device__ __forceinline__ bool list_entry(const PagesBlock& b, const int* dests, int i, int from, int to, bool fresh,
+                                           int* page, int* has) {
+    bool ok = to >= 0 && to < b.n_slots;
+    if (ok) {
+        *has = b.table[to];
+        ok = fresh ? *has == -1 : *has >= 0 && *has < b.n_pages;
+    }
+    *page = -1;
+    if (from != -1) {
+        ok = ok && from >= 0 && from < b.n_slots;
+        if (ok) *page = b.table[from];
+        ok = ok && *page >= 0 && *page < b.n_pages;
+    }
+    for (int m = 0; m < i; ++m) ok = ok && dests[m] != to;
+    if (!ok) atomicOr(b.err, kPagesBadSlot);
+    return ok;
+}
+
+constexpr int kFusedList = 256, kFusedPages = 4096, kPer = kFusedPages / kMoveThreads;
+struct FusedPlan {
+    int dests[kFusedList], slots[kFusedList];
+    int src[kFusedPages / 2], dst[kFusedPages / 2];
+};
+
+// True in the last block that gets here: the others have read all that it may now overwrite.
+__device__ __forceinline__ bool last_block(const PagesBlock& b) {
+    __shared__ bool last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(b.tickets, 1u) == gridDim.x - 1;
+        if (last) *b.tickets = 0;
+    }
+    __syncthreads();
+    return last;
+}
+
+__global__ void __launch_bounds__(kMoveThreads) pages_fork_kernel(PagesBlock b, const int* __restrict__ source,
+                                                                  const int* __restrict__ dest, int n, char* pool,
+                                                                  size_t page_bytes, long vecs) {
+    __shared__ FusedPlan plan;
+    const int i = threadIdx.x, to = i < n ? dest[i] : -1, from = i < n ? source[i] : -1;
+    // the free pages of this thread's stretch
+    const int per = (b.n_pages + kMoveThreads - 1) / kMoveThreads, p0 = i * per;
+    uint32_t open = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (k < per && p0 + k < b.n_pages && b.owner[p0 + k] == -1) open |= 1u << k;
+    plan.dests[i] = to;
+    __syncthreads();
+    int page, has, count, open_all;
+    const bool ok = to != -1 && list_entry(b, plan.dests, i, from, to, true, &page, &has);
+    const int r = block_sum(ok, &count);
+    if (ok) {
+        plan.src[r] = page;
+        plan.slots[r] = to;
+    }
+    int f = block_sum(__popc(open), &open_all);
+    const int moves = min(count, open_all);
+    for (; open && f < moves; open &= open - 1) plan.dst[f++] = p0 + __ffs(open) - 1;
+    __syncthreads();
+    if (pool) move_pages(plan.src, plan.dst, moves, pool, page_bytes, vecs);
+    if (!last_block(b)) return;
+    if (i < moves) {
+        b.table[plan.slots[i]] = plan.dst[i];
+        b.owner[plan.dst[i]] = plan.slots[i];
+    }
+    if (i == 0 && moves < count) atomicOr(b.err, kPagesFull);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) pages_compact_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs) {
+    __shared__ FusedPlan plan;
+    const int per = (b.n_pages + kMoveThreads - 1) / kMoveThreads, p0 = threadIdx.x * per;
+    uint32_t used = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (k < per && p0 + k < b.n_pages && b.owner[p0 + k] >= 0) used |= 1u << k;
+    int live, holes, late;
+    block_sum(__popc(used), &live);
+    const int here = min(max(b.n_pages - p0, 0), per);                     // pages of the stretch
+    const int low = min(max(live - p0, 0), here);                          // those before `live`
+    const uint32_t low_bits = low == 32 ? ~0u : (1u << low) - 1u;
+    uint32_t hole = ~used & low_bits, move = used & ~low_bits;
+    int h = block_sum(__popc(hole), &holes), l = block_sum(__popc(move), &late);
+    for (; hole; hole &= hole - 1) plan.dst[h++] = p0 + __ffs(hole) - 1;
+    for (; move; move &= move - 1) plan.src[l++] = p0 + __ffs(move) - 1;
+    __syncthreads();
+    move_pages(plan.src, plan.dst, late, pool, page_bytes, vecs);
+    if (!last_block(b)) return;
+    for (int r = threadIdx.x; r < late; r += kMoveThreads) {
+        const int from = plan.src[r], to = plan.dst[r], slot = b.owner[from];
+        b.owner[to] = slot;
+        b.owner[from] = -1;
+        if (slot < b.n_slots) b.table[slot] = to;
+        else atomicOr(b.err, kPagesBadSlot);
+    }
+}
+
+// Moves as if all at once: a block owns a strip of `width` 16-byte columns of every page, reads it
+// for all moves into shared memory, then writes it.
+__device__ __forceinline__ void move_strip(const int* src, const int* dst, int moves, char* pool, size_t page_bytes,
+                                           long vecs, int width, uint4* held) {
     const long c0 = (long)blockIdx.x * width;
-    const int w = (int)min((long)width, vecs - c0), total = *b.moves * w;
-    for (int i = threadIdx.x; i < total; i += 256) {
-        const int m = i / w;
-        const int from = b.src[m];
+    const int w = (int)min((long)width, vecs - c0), total = moves * w;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < total; i += kMoveThreads) {
+        const int from = src[i / w];
         held[i] = from < 0 ? make_uint4(0, 0, 0, 0)
                            : *reinterpret_cast<const uint4*>(pool + (size_t)from * page_bytes + (c0 + i % w) * 16);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < total; i += 256) {
-        const int m = i / w;
-        *reinterpret_cast<uint4*>(pool + (size_t)b.dst[m] * page_bytes + (c0 + i % w) * 16) = held[i];
+#pragma unroll 4
+    for (int i = threadIdx.x; i < total; i += kMoveThreads)
+        *reinterpret_cast<uint4*>(pool + (size_t)dst[i / w] * page_bytes + (c0 + i % w) * 16) = held[i];
+}
+
+__global__ void __launch_bounds__(kMoveThreads) pages_strip_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs,
+                                                                   int width) {
+    extern __shared__ uint4 held[];
+    move_strip(b.src, b.dst, *b.moves, pool, page_bytes, vecs, width, held);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) pages_copy_kernel(PagesBlock b, const int* __restrict__ source,
+                                                                  const int* __restrict__ dest, int n, char* pool,
+                                                                  size_t page_bytes, long vecs, int width) {
+    extern __shared__ uint4 held[];
+    __shared__ int dests[kFusedList], src[kFusedList], dst[kFusedList];
+    const int i = threadIdx.x, to = i < n ? dest[i] : -1, from = i < n ? source[i] : -1;
+    dests[i] = to;
+    __syncthreads();
+    int page, has, moves;
+    bool ok = to != -1 && list_entry(b, dests, i, from, to, false, &page, &has);
+    ok = ok && from != to;
+    const int r = block_sum(ok, &moves);
+    if (ok) {
+        src[r] = page;
+        dst[r] = has;
     }
+    __syncthreads();
+    move_strip(src, dst, moves, pool, page_bytes, vecs, width, held);
 }
 
 // Rows into the pages of their slots (write) or out of them; one block per 4 KiB of a row.
@@ -265,12 +433,25 @@ static cudaError_t launch_moves(const PagesBlock& b, void* pool, size_t page_byt
                                 cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    pages_move_kernel<<<move_grid(), 256, 0, stream>>>(b, static_cast<char*>(pool), page_bytes, (long)(data_bytes / 16));
+    pages_move_kernel<<<move_grid(), kMoveThreads, 0, stream>>>(b, static_cast<char*>(pool), page_bytes,
+                                                                (long)(data_bytes / 16));
     return cudaGetLastError();
+}
+
+// A fused call's blocks: what its largest possible number of moves keeps busy.
+static unsigned fused_grid(long moves, long vecs) {
+    const long pieces = moves * ((vecs + kUnit - 1) / kUnit), most = move_grid();
+    return (unsigned)(pieces < 1 ? 1 : pieces < most ? pieces : most);
 }
 
 cudaError_t launch_pages_fork(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes, const int* source,
                               const int* dest, int n, cudaStream_t stream) {
+    const long vecs = pool ? (long)(data_bytes / 16) : 0;
+    if (n <= kFusedList && b.n_pages <= kFusedPages) {
+        pages_fork_kernel<<<fused_grid(n, vecs), kMoveThreads, 0, stream>>>(b, source, dest, n, static_cast<char*>(pool),
+                                                                            page_bytes, vecs);
+        return cudaGetLastError();
+    }
     pages_fork_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
     if (!pool) return cudaGetLastError();
     return launch_moves(b, pool, page_bytes, data_bytes, stream);
@@ -278,22 +459,38 @@ cudaError_t launch_pages_fork(const PagesBlock& b, void* pool, size_t page_bytes
 
 cudaError_t launch_pages_compact(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes,
                                  cudaStream_t stream) {
+    if (b.n_pages <= kFusedPages) {
+        const long vecs = (long)(data_bytes / 16);
+        pages_compact_kernel<<<fused_grid(b.n_pages / 2, vecs), kMoveThreads, 0, stream>>>(b, static_cast<char*>(pool),
+                                                                                         page_bytes, vecs);
+        return cudaGetLastError();
+    }
     pages_compact_plan<<<1, kPlanThreads, 0, stream>>>(b);
     return launch_moves(b, pool, page_bytes, data_bytes, stream);
 }
 
 cudaError_t launch_pages_copy(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes, const int* source,
                               const int* dest, int n, cudaStream_t stream) {
-    pages_copy_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    // strips as wide as shared memory allows, but enough of them for every SM (down to 128 bytes)
+    const long vecs = (long)(data_bytes / 16), spread = (vecs + 295) / 296;
+    long width = kPagesCopyMax / n;
+    if (width > (spread > 8 ? spread : 8)) width = spread > 8 ? spread : 8;
+    if (width > vecs) width = vecs;
+    const unsigned grid = (unsigned)((vecs + width - 1) / width);
+    const size_t held = (size_t)n * width * 16;
     constexpr int kHeld = kPagesCopyMax * 16;
-    static std::atomic<uint64_t> done{0};
+    static std::atomic<uint64_t> done{0}, done_list{0};
+    cudaError_t e;
+    if (n <= kFusedList) {
+        if ((e = set_smem_limit_once(pages_copy_kernel, kHeld, done_list)) != cudaSuccess) return e;
+        pages_copy_kernel<<<grid, kMoveThreads, held, stream>>>(b, source, dest, n, static_cast<char*>(pool), page_bytes,
+                                                                vecs, (int)width);
+        return cudaGetLastError();
+    }
+    pages_copy_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = set_smem_limit_once(pages_strip_kernel, kHeld, done)) != cudaSuccess) return e;
-    const long vecs = (long)(data_bytes / 16);
-    const int width = (int)(vecs < kPagesCopyMax / n ? vecs : kPagesCopyMax / n);
-    pages_strip_kernel<<<(unsigned)((vecs + width - 1) / width), 256, (size_t)n * width * 16, stream>>>(
-        b, static_cast<char*>(pool), page_bytes, vecs, width);
+    pages_strip_kernel<<<grid, kMoveThreads, held, stream>>>(b, static_cast<char*>(pool), page_bytes, vecs, (int)width);
     return cudaGetLastError();
 }
 

@@ -9,7 +9,7 @@
 
 namespace efla {
 
-// The block, in int32 words: a header of 64 (word 0: errors, word 1: moves of the running call),
+// The block, in int32 words: a header of 64 (word 0: errors, 1 and 2: the running call's),
 // the table (slot -> page), the owners (page -> slot), then scratch: a claim per slot (zero
 // between calls) and the list of page moves.
 constexpr int kPagesHeader = 64;
@@ -17,6 +17,7 @@ enum : uint32_t { kPagesBadSlot = 4u, kPagesFull = 8u };   // error word bits
 struct PagesBlock {
     uint32_t* err;
     int* moves;
+    uint32_t* tickets;     // blocks of the running call that are done; zero between calls
     int* table;
     int* owner;
     int* claim;
@@ -32,6 +33,7 @@ inline PagesBlock pages_block(void* p, int n_pages, int n_slots) {
     PagesBlock b;
     b.err = reinterpret_cast<uint32_t*>(w);
     b.moves = w + 1;
+    b.tickets = reinterpret_cast<uint32_t*>(w + 2);
     b.table = w + kPagesHeader;
     b.owner = b.table + n_slots;
     b.claim = b.owner + n_pages;

@@ -764,6 +764,12 @@ double scan_cost(long strips, long steps, int groups, int blocks, long held, lon
 // three blocks each.  (64 heads of 128, T 2048: 37.5 us at width 128 with four blocks, 34 at 32 with
 // one; 16 heads, T 32768: 263 us at 128 with eight, 133 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
 Geo scan_geo(long Z, int T, int d) {
+    static thread_local struct {
+        long Z;
+        int T, d;
+        Geo geo;
+    } before{-1, 0, 0, {}};          // (a call asks for its sizes several times)
+    if (before.Z == Z && before.T == T && before.d == d) return before.geo;
     Geo best{};
     double least = 0;
     for (int groups = 1; groups <= 4; groups *= 2) {
@@ -783,6 +789,7 @@ Geo scan_geo(long Z, int T, int d) {
         }
         if (groups == 1 || cost < least) best = G, least = cost;
     }
+    before = {Z, T, d, best};
     return best;
 }
 
