@@ -518,7 +518,7 @@ def _tensor(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optio
     """The address of a contiguous tensor of this type, device and shape (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.device == device and t.shape == shape and t.is_contiguous():
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -555,30 +555,36 @@ def efla_scan_workspace_bytes(B, H, T, d, g_width, dtype=torch.bfloat16, packed:
     return int(lib.efla_scan_workspace_bytes(B, H, T, d, g_width, _DTYPES.get(dtype, -1), int(packed)))
 
 
-def _scan_workspace(n: int, device, where: str):
-    if n == 0:
-        raise EflaError(EFLA_ERR_UNSUPPORTED, where)
-    w = torch.empty(n, dtype=torch.uint8, device=device)
-    w[:4].zero_()
-    return w
-
-
 def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule, keep):
     B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
-    dev = x.device
-    px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", torch.float32, dev, g.shape)
-    pS0 = _tensor(S0, "S0", torch.float32, dev, (B, H, d))
+    dev, f32 = x.device, torch.float32
+    if dev.index is None:
+        raise ValueError(f"x must be on a CUDA device, got {dev}")
+    px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", f32, dev, g.shape)
+    pS0 = _tensor(S0, "S0", f32, dev, (B, H, d))
     if o is None:
         o = torch.empty_like(x)
+        po = o.data_ptr()
+    else:
+        po = _tensor(o, "o", x.dtype, dev, x.shape)
     if S_T is None and want_state:
-        S_T = torch.empty((B, H, d), device=dev, dtype=torch.float32)
+        S_T = x.new_empty((B, H, d), dtype=f32)
+        pS_T = S_T.data_ptr()
+    else:
+        pS_T = _tensor(S_T, "S_T", f32, dev, (B, H, d))
     if workspace is None:
         n = lib.efla_scan_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None))
-        workspace = (_scan_workspace(n, dev, "efla_scan_workspace_bytes") if keep or not n else
-                     torch.empty(n, dtype=torch.uint8, device=dev))
-    _call(lib.efla_scan_fwd, "efla_scan_fwd", dev, stream, px, pg, None if cu is None else cu.data_ptr(), pS0,
-          _tensor(o, "o", x.dtype, dev, x.shape), _tensor(S_T, "S_T", torch.float32, dev, (B, H, d)), B, H, T, d, gw,
-          dt, int(rule), _tensor(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)), workspace.numel())
+        if n == 0:
+            raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_workspace_bytes")
+        workspace = x.new_empty(n, dtype=torch.uint8)
+        if keep:
+            workspace[:4].zero_()       # the error word, for efla_workspace_status
+        pw = workspace.data_ptr()
+    else:
+        n = workspace.numel()
+        pw = _tensor(workspace, "workspace", torch.uint8, dev, (n,))
+    _call(lib.efla_scan_fwd, "efla_scan_fwd", dev, stream, px, pg, None if cu is None else cu.data_ptr(), pS0, po, pS_T,
+          B, H, T, d, gw, dt, int(rule), pw, n)
     return o, S_T, workspace
 
 
@@ -605,22 +611,27 @@ def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None
     (None: computed again).  `grads` may supply the three tensors preallocated (dS0 may be None)."""
     B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
     dev, f32 = x.device, torch.float32
+    px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", f32, dev, g.shape)
+    pS0, pdO = _tensor(S0, "S0", f32, dev, (B, H, d)), _tensor(dO, "dO", x.dtype, dev, x.shape)
+    pdS_T = _tensor(dS_T, "dS_T", f32, dev, (B, H, d))
     if grads is None:
-        grads = (torch.empty(x.shape, device=dev, dtype=f32), torch.empty(g.shape, device=dev, dtype=f32),
-                 torch.empty((B, H, d), device=dev, dtype=f32) if want_dS0 else None)
+        grads = (torch.empty_like(x, dtype=f32), torch.empty_like(g),
+                 x.new_empty((B, H, d), dtype=f32) if want_dS0 else None)
+        out = [None if t is None else t.data_ptr() for t in grads]
+    else:
+        out = [_tensor(t, name, f32, dev, shape)
+               for t, name, shape in zip(grads, ("dx", "dg", "dS0"), (x.shape, g.shape, (B, H, d)))]
     if workspace is None:
         n = lib.efla_scan_backward_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None), int(saved is not None))
         if n == 0:
             raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_backward_workspace_bytes")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _call(lib.efla_scan_backward, "efla_scan_backward", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
-          _tensor(g, "g", f32, dev, g.shape), None if cu is None else cu.data_ptr(),
-          _tensor(S0, "S0", f32, dev, (B, H, d)), _tensor(dO, "dO", x.dtype, dev, x.shape),
-          _tensor(dS_T, "dS_T", f32, dev, (B, H, d)), _tensor(grads[0], "dx", f32, dev, x.shape),
-          _tensor(grads[1], "dg", f32, dev, g.shape), _tensor(grads[2], "dS0", f32, dev, (B, H, d)), B, H, T, d, gw, dt,
-          int(rule), None if saved is None else _tensor(saved, "saved", torch.uint8, dev, (saved.numel(),)),
-          0 if saved is None else saved.numel(), _tensor(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)),
-          workspace.numel())
+        workspace = x.new_empty(n, dtype=torch.uint8)
+    else:
+        n = workspace.numel()
+    ns = 0 if saved is None else saved.numel()
+    _call(lib.efla_scan_backward, "efla_scan_backward", dev, stream, px, pg, None if cu is None else cu.data_ptr(), pS0,
+          pdO, pdS_T, *out, B, H, T, d, gw, dt, int(rule), _tensor(saved, "saved", torch.uint8, dev, (ns,)), ns,
+          _tensor(workspace, "workspace", torch.uint8, dev, (n,)), n)
     return grads
 
 
