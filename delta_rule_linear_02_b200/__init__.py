@@ -514,6 +514,23 @@ def _call(fn, where: str, device: torch.device, stream, *args):
         raise EflaError(status, where)
 
 
+def _made_here(stream, *tensors) -> None:
+    """Tensors that a call allocated itself and uses on `stream`: their memory is not given away before it has run."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _zeros(like: torch.Tensor, shape, stream) -> torch.Tensor:
+    """Zeros made on `stream` (None: the current one), so that the call that fills them comes after."""
+    if stream is None:
+        return like.new_zeros(shape)
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+        return like.new_zeros(shape)
+
+
 def _tensor(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optional[int]:
     """The address of a contiguous tensor of this type, device and shape (None: NULL)."""
     if t is None:
@@ -555,7 +572,7 @@ def efla_scan_workspace_bytes(B, H, T, d, g_width, dtype=torch.bfloat16, packed:
     return int(lib.efla_scan_workspace_bytes(B, H, T, d, g_width, _DTYPES.get(dtype, -1), int(packed)))
 
 
-def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule, keep):
+def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule):
     B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
     dev, f32 = x.device, torch.float32
     if dev.index is None:
@@ -565,11 +582,13 @@ def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule,
     if o is None:
         o = torch.empty_like(x)
         po = o.data_ptr()
+        _made_here(stream, o)
     else:
         po = _tensor(o, "o", x.dtype, dev, x.shape)
     if S_T is None and want_state:
         S_T = x.new_empty((B, H, d), dtype=f32)
         pS_T = S_T.data_ptr()
+        _made_here(stream, S_T)
     else:
         pS_T = _tensor(S_T, "S_T", f32, dev, (B, H, d))
     if workspace is None:
@@ -577,9 +596,8 @@ def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule,
         if n == 0:
             raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_workspace_bytes")
         workspace = x.new_empty(n, dtype=torch.uint8)
-        if keep:
-            workspace[:4].zero_()       # the error word, for efla_workspace_status
         pw = workspace.data_ptr()
+        _made_here(stream, workspace)
     else:
         n = workspace.numel()
         pw = _tensor(workspace, "workspace", torch.uint8, dev, (n,))
@@ -594,14 +612,14 @@ def efla_scan_fwd(x, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspace=No
     x [B,H,T,d] float32 or bfloat16; g float32, x's shape or [B,H,T] (one decay per head); S0 [B,H,d] float32 or
     None.  Packed: cu_seqlens (B + 1 offsets, ints or a CPU int32 tensor) with x [H,T,d], g [H,T,d] or [H,T].
     Returns (o like x, S_T [B,H,d] float32 or None)."""
-    return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule, False)[:2]
+    return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule)[:2]
 
 
 def efla_scan_fwd_save(x, g, S0=None, cu_seqlens=None, saved=None, o=None, S_T=None, want_state: bool = True,
                        stream=None, rule: int = EFLA_RULE_EXACT):
     """efla_scan_fwd that also returns what efla_scan_backward starts from: (o, S_T or None, saved); `saved` is a
     uint8 tensor of efla_scan_workspace_bytes."""
-    return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, saved, want_state, stream, rule, True)
+    return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, saved, want_state, stream, rule)
 
 
 def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None, want_dS0: bool = True, grads=None,
@@ -618,6 +636,7 @@ def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None
         grads = (torch.empty_like(x, dtype=f32), torch.empty_like(g),
                  x.new_empty((B, H, d), dtype=f32) if want_dS0 else None)
         out = [None if t is None else t.data_ptr() for t in grads]
+        _made_here(stream, *grads)
     else:
         out = [_tensor(t, name, f32, dev, shape)
                for t, name, shape in zip(grads, ("dx", "dg", "dS0"), (x.shape, g.shape, (B, H, d)))]
@@ -626,6 +645,7 @@ def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None
         if n == 0:
             raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_backward_workspace_bytes")
         workspace = x.new_empty(n, dtype=torch.uint8)
+        _made_here(stream, workspace)
     else:
         n = workspace.numel()
     ns = 0 if saved is None else saved.numel()
@@ -651,6 +671,7 @@ def efla_scan_step(x, g, S, o=None, stream=None, rule: int = EFLA_RULE_EXACT) ->
     dev = x.device
     if o is None:
         o = torch.empty_like(x)
+        _made_here(stream, o)
     _call(lib.efla_scan_step, "efla_scan_step", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
           _tensor(g, "g", torch.float32, dev, g.shape), _tensor(S, "S", torch.float32, dev, x.shape),
           _tensor(o, "o", x.dtype, dev, x.shape), N, H, d, gw, dt, int(rule))
@@ -690,6 +711,7 @@ def new_pages(n_pages: int, n_slots: int, device="cuda", stream=None) -> EflaPag
     if n == 0:
         raise EflaError(EFLA_ERR_INVALID_ARG, "efla_pages_bytes")
     pages = EflaPages(torch.empty(n // 4, dtype=torch.int32, device=device), n_pages, n_slots)
+    _made_here(stream, pages.block)
     _call(lib.efla_pages_init, "efla_pages_init", pages.block.device, stream, pages.block.data_ptr(), n, n_pages,
           n_slots)
     return pages
@@ -764,7 +786,7 @@ def efla_pages_read(pages: EflaPages, pool, slots: torch.Tensor, rows: Optional[
                     stream=None) -> torch.Tensor:
     """The pages of slots[i] as rows [n, ...] (zero rows for padding when `rows` is not given)."""
     if rows is None:
-        rows = torch.zeros((slots.numel(), *pool.shape[1:]), dtype=pool.dtype, device=pool.device)
+        rows = _zeros(pool, (slots.numel(), *pool.shape[1:]), stream)
     _pages_rows(lib.efla_pages_read, "efla_pages_read", pages, pool, rows, slots, stream)
     return rows
 
@@ -789,7 +811,7 @@ def efla_scan_step_paged(x, g, pages: EflaPages, pool, slots, source=None, o=Non
         raise ValueError(f"pool must be [{pages.n_pages},{H},{d}], got {tuple(pool.shape)}")
     ptr, stride, _ = _pool(pool, pages, torch.float32)
     if o is None:
-        o = torch.zeros_like(x)
+        o = _zeros(x, x.shape, stream)
     _call(lib.efla_scan_step_paged, "efla_scan_step_paged", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
           _tensor(g, "g", torch.float32, dev, g.shape), pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr, stride,
           _slots(slots, "slots", dev, N), _slots(source, "source", dev, N), _tensor(o, "o", x.dtype, dev, x.shape), N, H,
@@ -810,7 +832,7 @@ def efla_recurrent_step_paged(q, k, v, beta, pages: EflaPages, pool, slots, sour
         raise ValueError(f"pool must be [{pages.n_pages},{H},{d_k},{d_v}], got {tuple(pool.shape)}")
     ptr, stride, _ = _pool(pool, pages, torch.float32)
     if o is None:
-        o = torch.zeros_like(v)
+        o = _zeros(v, v.shape, stream)
     _call(lib.efla_recurrent_step_paged, "efla_recurrent_step_paged", dev, stream, _tensor(q, "q", dt, dev, k.shape),
           _tensor(k, "k", dt, dev, k.shape), _tensor(v, "v", dt, dev, (N, H, d_v)), _tensor(beta, "beta", dt, dev, (N, H)),
           _tensor(g, "g", torch.float32, dev, (N, H)), pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr, stride,

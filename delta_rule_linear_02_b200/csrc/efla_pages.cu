@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kMoveThreads) pages_compact_kernel(PagesBlock 
     block_sum(__popc(used), &live);
     const int here = min(max(b.n_pages - p0, 0), per);                     // pages of the stretch
     const int low = min(max(live - p0, 0), here);                          // those before `live`
-    const uint32_t low_bits = low == 32 ? ~0u : (1u << low) - 1u;
+    const uint32_t low_bits = (1u << low) - 1u;
     uint32_t hole = ~used & low_bits, move = used & ~low_bits;
     int h = block_sum(__popc(hole), &holes), l = block_sum(__popc(move), &late);
     for (; hole; hole &= hole - 1) plan.dst[h++] = p0 + __ffs(hole) - 1;

@@ -278,7 +278,7 @@ __device__ __forceinline__ float2 chain_turn(const Fold& f, int blocks, const Ge
         wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
     }
     float2 mine = h;
-#pragma unroll 4
+#pragma unroll 8
     for (int q = 0; q < entries; ++q) {
         const float4 v = all[q * row + pair];
         if (q == entry) mine = h;
@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
     const int rank = blocks > 1 ? (int)cluster_rank() : 0;
     const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
     if (threadIdx.x == 0) {
+        if (P.clear_err && blockIdx.x == 0) *P.err = kDevOk;
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
         mbar_init(ready, kWarps);
         mbar_init(entered, kChainThreads / 32);
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     const int rank = blocks > 1 ? (int)cluster_rank() : 0;
     const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
     if (threadIdx.x == 0) {
+        if (P.clear_err && blockIdx.x == 0) *P.err = kDevOk;
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1), mbar_init(spent + i, kWarps);
         mbar_init(ready, kWarps);
         mbar_init(entered, kChainThreads / 32);

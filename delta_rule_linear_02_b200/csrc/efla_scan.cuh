@@ -120,6 +120,7 @@ struct ScanArgs {
     float* dS0 = nullptr;
     void* scratch = nullptr;
     uint32_t* err = nullptr;
+    bool clear_err = true;          // the first kernel of a call forgets the last call's errors
 };
 size_t scan_states_bytes(long Z, int T, int d);
 size_t scan_scratch_bytes(long Z, int T, int d, int gw, bool backward);

@@ -41,7 +41,7 @@ int check_scan_shape(int B, int H, int T, int d, int g_width, int dtype) {
     if (B < 0 || H < 0 || T < 0 || d <= 0) return EFLA_ERR_INVALID_ARG;
     if (dtype != EFLA_DTYPE_F32 && dtype != EFLA_DTYPE_BF16) return EFLA_ERR_UNSUPPORTED;
     if (g_width != 1 && g_width != d) return EFLA_ERR_INVALID_ARG;
-    if (d > 4096 || (d * elem_size(dtype)) % 16 != 0) return EFLA_ERR_UNSUPPORTED;
+    if (d > 4096 || (d * elem_size(dtype)) % 16 != 0 || T > (1 << 30)) return EFLA_ERR_UNSUPPORTED;
     if ((long long)B * H * ((d + 127) / 128) >= (1ll << 31)) return EFLA_ERR_UNSUPPORTED;
     return EFLA_OK;
 }
@@ -177,6 +177,7 @@ int efla_scan_backward(const void* x, const float* g, const int* cu_seqlens, con
         a.scratch = ws + kHeader + cu_bytes(B, packed) + efla::scan_states_bytes(Z, T, d);
         const cudaError_t e = efla::launch_scan_fwd(a, bf16, s);
         if (e != cudaSuccess) return EFLA_ERR_CUDA;
+        a.clear_err = false;
     }
     a.scratch = ws + (saved ? 0 : fwd) + kHeader;
     a.dO = dO;

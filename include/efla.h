@@ -416,12 +416,14 @@ int efla_backward_saved(const void *q, const void *k, const void *v, const void 
  * Packed batches: with cu_seqlens (a HOST array of B + 1 offsets as in efla_chunk_fwd_varlen, T =
  * cu_seqlens[B]) the tensors are [H,T,d], [H,T,(d)] and every sequence runs from its own S0 row;
  * an empty one passes its state through.  The offsets are copied to the workspace (from pageable
- * memory that copy may synchronise the host with `stream`, and it cannot be captured).
- * Supported: d up to 4096 with d * sizeof(dtype) a multiple of 16 bytes; any T >= 0 and B, H >= 0.
+ * memory that copy may synchronise the host with `stream`, and it cannot be captured; from pinned
+ * memory they have to stay as they are until the call has run).
+ * Supported: d up to 4096 with d * sizeof(dtype) a multiple of 16 bytes; 0 <= T <= 2^30, B, H >= 0.
  *
  * efla_scan_workspace_bytes -- workspace of efla_scan_fwd (packed != 0: with cu_seqlens), 0 for
- * arguments it would reject.  Its first bytes hold a sticky device error word (a wait that ran out;
- * efla_workspace_status; zero it once before first use if it is to be read).
+ * arguments it would reject.  It needs no preparation.  Its first bytes hold the device error word
+ * of the last call that used it (a wait that ran out; read it with efla_workspace_status).  Calls
+ * that overlap on the GPU must not share a workspace.
  *
  * efla_scan_fwd -- the forward.  S0 NULL: zero states.  S_T may be NULL (not wanted) or alias S0;
  * otherwise no output may overlap an input, the workspace or another output.  All pointers
@@ -467,9 +469,11 @@ int efla_scan_step(const void *x, const float *g, float *S, void *o, int N, int 
  *          of 16).  A call works on data_bytes of each page from `pool` on, so that a page may
  *          hold several layers and a step is given the pool at its layer's offset.
  *   pages  the block, efla_pages_bytes(n_pages, n_slots) bytes, 16-byte aligned, in int32 words:
- *          64 of header (word 0: errors), n_slots of table (slot -> page, -1: none), n_pages of
- *          owners (page -> slot, -1: free), then scratch (zero between calls as efla_pages_init
- *          leaves it).
+ *          64 of header (word 0: errors, the others zero between calls), n_slots of table (slot ->
+ *          page, -1: none), n_pages of owners (page -> slot, -1: free), then scratch: n_slots words
+ *          that are zero between calls and 2 * n_pages of any content.  efla_pages_init writes all
+ *          of it; a program may read the table and owners, and write them if it keeps them
+ *          consistent (page p of slot s: table[s] = p and owner[p] = s).
  * Lists of slots are int32 device arrays; an entry -1 is padding and skipped.  The calls plan on
  * the device: they never synchronise, can be captured and replayed, and give the same result on
  * every run.  Calls on one block have to be ordered by streams or events.
@@ -493,7 +497,8 @@ int efla_scan_step(const void *x, const float *g, float *S, void *o, int N, int 
  *   them (a prefill's final states into the cache, a sequence's state out to elsewhere); rows of
  *   entries that are left out are not touched.  row_bytes is the call's data_bytes.
  * efla_pages_status -- waits for `stream` and reports the errors of the calls so far (clear != 0:
- *   forgets them).  The only call that synchronises the host.
+ *   forgets them): EFLA_ERR_TIMEOUT (a device wait of a paged step ran out; its states are then
+ *   invalid) before EFLA_ERR_SLOT before EFLA_ERR_FULL.  The only call that synchronises the host.
  */
 size_t efla_pages_bytes(int n_pages, int n_slots);
 int efla_pages_init(void *pages, size_t pages_bytes, int n_pages, int n_slots, efla_stream_t stream);

@@ -247,8 +247,7 @@ def test_empty_calls(efla, cuda):
 def test_workspace_reuse_across_shapes_and_garbage(efla, cuda):
     """A workspace left with anything in it, or used by a call of another shape, changes nothing."""
     ws = torch.full((1 << 22,), 0xA5, dtype=torch.uint8, device="cuda")
-    ws[:256] = 0
-    for T, H, d in ((300, 2, 64), (77, 3, 128), (2000, 1, 64), (33, 2, 64)):
+    for T, H, d in ((300, 2, 64), (77, 3, 128), (2000, 1, 64), (33, 2, 64), (700, 20, 128)):
         inp = inputs(1, H, T, d, torch.float32, True, seed=T)
         dd = dev(inp)
         o, S_T = efla.efla_scan_fwd(dd["x"], dd["g"], S0=dd["S0"], workspace=ws)
@@ -272,10 +271,17 @@ def test_streams_and_graphs(efla, cuda):
         torch.cuda.synchronize()
         for (o, S), (o2, S2) in zip(want, got):
             assert torch.equal(o, o2) and torch.equal(S, S2)
-    # explicit stream argument
-    o2, S2 = efla.efla_scan_fwd(a["x"], a["g"], S0=a["S0"], stream=streams[0])
-    torch.cuda.synchronize()
-    assert torch.equal(o2, want[0][0])
+    # a stream as an argument, an object or an address; what the calls allocate is theirs until they have run
+    for stream in (streams[0], streams[1].cuda_stream):
+        outs = [efla.efla_scan_fwd(a["x"], a["g"], S0=a["S0"], stream=stream) for _ in range(3)]
+        _, _, saved = efla.efla_scan_fwd_save(a["x"], a["g"], S0=a["S0"], stream=stream)
+        grads = efla.efla_scan_backward(a["x"], a["g"], a["dO"], S0=a["S0"], dS_T=a["dS_T"], saved=saved, stream=stream)
+        for _ in range(20):
+            torch.empty(1 << 22, device="cuda").fill_(float("nan"))      # would land in memory freed too early
+        torch.cuda.synchronize()
+        assert all(torch.equal(o2, want[0][0]) and torch.equal(S2, want[0][1]) for o2, S2 in outs)
+        ref = efla.efla_scan_backward(a["x"], a["g"], a["dO"], S0=a["S0"], dS_T=a["dS_T"])
+        assert all(torch.equal(u, v) for u, v in zip(grads, ref))
     t = {k: v.clone() for k, v in a.items()}
 
     def train():

@@ -131,9 +131,10 @@ def test_wrong_entries_touch_nothing(efla, cuda):
 def test_random_calls(efla, cuda):
     import random
     r = random.Random(5)
-    for n_pages, n_slots in ((37, 50), (1100, 1200)):
+    # lists and caches below and above what one launch plans (256 entries, 4096 pages)
+    for n_pages, n_slots, rounds in ((37, 50, 12), (1100, 1200, 12), (4096, 300, 6), (4500, 5000, 6)):
         b = Both(efla, n_pages, n_slots, (12,), seed=n_pages)
-        for _ in range(12):
+        for _ in range(rounds):
             pick = lambda k: [r.randrange(-1, n_slots) for _ in range(k)]
             k = r.choice([1, 5, n_slots // 2, n_slots + 30])
             b.fork(pick(k), pick(k))
@@ -282,6 +283,38 @@ def test_paged_step_is_the_dense_step(efla, cuda):
     S2 = torch.stack([b.pool[b.ref.table[s]] for s in slots])
     # the same formulas in the same precision: a few roundings apart
     assert float((S - S2).abs().max()) <= 1e-5 and float((o1.float() - o2.float()).abs().max()) <= 2e-2
+
+
+def test_full_cache_many_entries(efla, cuda):
+    """More entries than free pages, by both planners: the first entries get them."""
+    for n_pages, n in ((10, 100), (300, 600), (5000, 5200)):
+        b = Both(efla, n_pages, n, (4,))
+        b.fork([-1] * n, list(range(n)))
+        b.check(efla.EFLA_ERR_FULL)
+        b.free(list(range(0, n_pages, 3)))
+        b.compact()
+        b.check(efla.EFLA_OK)
+
+
+def test_other_streams(efla, cuda):
+    """Calls on streams of their own, with outputs that they allocate."""
+    N, H, d = 6, 2, 64
+    b = filled(efla, 8, 8, 8, (H, d, d))
+    v = filled(efla, 8, 8, 8, (H, d))
+    c = {n: t.cuda() for n, t in step_case(N, H, d, torch.float32, 3).items()}
+    slots = ints([5, 0, -1, 2, 1, 3])
+    want = None
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        pool, vec = b.pool.clone(), v.pool.clone()
+        torch.cuda.synchronize()
+        o1 = efla.efla_recurrent_step_paged(c["q"], c["k"], c["v"], c["beta"], b.pages, pool, slots, stream=stream)
+        o2 = efla.efla_scan_step_paged(c["x"], c["gx"], v.pages, vec, slots, stream=stream)
+        rows = efla.efla_pages_read(v.pages, vec, slots, stream=stream)
+        torch.cuda.synchronize()
+        got = (o1, o2, rows, pool, vec)
+        want = want or got
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        assert float(o1[2].abs().max()) == 0 and float(rows[2].abs().max()) == 0
 
 
 def test_far_pages(efla, cuda):

@@ -33,7 +33,7 @@ def test_scan_fwd(efla):
     for name in ("x", "g", "S0", "o", "S_T", "ws"):
         at = dict(x=P[0], g=P[1], S0=P[2], o=P[3], S_T=P[4], ws=P[5])[name]
         assert fwd(L, **{name: off(at)}) == INVALID, name
-    for bad in (dict(dt=2), dict(d=62), dict(d=4100), dict(d=4, dt=BF16), dict(d=12, dt=BF16), dict(H=1 << 16, B=1 << 16)):
+    for bad in (dict(dt=2), dict(T=(1 << 30) + 1), dict(d=62), dict(d=4100), dict(d=4, dt=BF16), dict(d=12, dt=BF16), dict(H=1 << 16, B=1 << 16)):
         assert fwd(L, **bad) == UNSUPPORTED, bad
     assert fwd(L, B=0) == OK and fwd(L, H=0) == OK
     need = L.efla_scan_workspace_bytes(2, 3, 70, 64, 64, F32, 0)
