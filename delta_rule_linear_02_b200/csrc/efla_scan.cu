@@ -278,7 +278,7 @@ __device__ __forceinline__ float2 chain_turn(const Fold& f, int blocks, const Ge
         wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
     }
     float2 mine = h;
-#pragma unroll 8
+#pragma unroll 4
     for (int q = 0; q < entries; ++q) {
         const float4 v = all[q * row + pair];
         if (q == entry) mine = h;
