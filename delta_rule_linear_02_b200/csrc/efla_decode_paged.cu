@@ -227,11 +227,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) decode_stream_kernel(const 
                 }
                 __syncwarp();
             } else {
-                // (a last job of fewer heads is shorter: then its quarters are not where the next one's go)
-                const bool same = jobs[b].heads == heads;
+                // A last job of fewer heads is shorter: then its quarters are not where the next one's go.  A
+                // job from a zero state loads none, and the workers may write theirs as soon as it begins.
+                const bool whole = jobs[b].heads != heads || pg.read < 0;
                 write_back(sent - kRing, [&](int) {
+                    if (whole) wait_read<0>();
                     begin();
-                    if (!same) wait_read<0>();
                     wait_read<3>();
                     load(0);
                     wait_read<2>();

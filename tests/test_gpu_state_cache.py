@@ -236,6 +236,31 @@ def test_paged_steps(efla, cuda, N, H, d, kind, dtype, rule):
                 assert torch.equal(o[n], marker[n])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,H,d", [(130, 7, 128), (480, 7, 64)])
+def test_paged_delta_step_of_many_rows(efla, cuda, N, H, d, dtype):
+    """Enough heads that every block takes many: rows from their own page, from another one and from a zero state in
+    turn, and heads that do not fill a block's last piece of a row."""
+    b = filled(efla, N + 9, N + 8, N + 8, (H, d, d), seed=d)
+    c = step_case(N, H, d, DT[dtype], d)
+    slots = torch.randperm(N, generator=torch.Generator().manual_seed(N)).tolist()
+    source = [-1 if n % 3 == 0 else s if n % 3 == 1 else N + n % 8 for n, s in enumerate(slots)]
+    dv = {n: t.cuda() for n, t in c.items()}
+    o = efla.efla_recurrent_step_paged(dv["q"], dv["k"], dv["v"], dv["beta"], b.pages, b.pool, ints(slots),
+                                       source=ints(source), g=dv["g"])
+    assert efla.efla_pages_status(b.pages) == efla.EFLA_OK
+    rows = pages_of(b.ref, slots, source)
+    assert len(rows) == N
+    S = torch.stack([torch.zeros(H, d, d) if s is None else s for _, _, s in rows])
+    ov, Sv, oe, Se = delta_step(c["q"], c["k"], c["v"], c["beta"], c["g"], S, EXACT)
+    close(o, (ov, oe), "o")
+    pages = [p for _, p, _ in rows]
+    after = b.pool.cpu()
+    close(after[pages], (Sv, Se), "states")
+    others = [p for p in range(N + 9) if p not in pages]
+    assert torch.equal(after[others], b.ref.pool[others])
+
+
 @pytest.mark.parametrize("H", [2, 150])
 @pytest.mark.parametrize("kind", ["delta", "scan"])
 def test_paged_steps_refuse_rows(efla, cuda, kind, H):
