@@ -42,7 +42,7 @@ int check_scan_shape(int B, int H, int T, int d, int g_width, int dtype) {
     if (dtype != EFLA_DTYPE_F32 && dtype != EFLA_DTYPE_BF16) return EFLA_ERR_UNSUPPORTED;
     if (g_width != 1 && g_width != d) return EFLA_ERR_INVALID_ARG;
     if (d > 4096 || (d * elem_size(dtype)) % 16 != 0 || T > (1 << 30)) return EFLA_ERR_UNSUPPORTED;
-    if ((long long)B * H * ((d + 127) / 128) >= (1ll << 31)) return EFLA_ERR_UNSUPPORTED;
+    if ((long long)B * H * ((d + 31) / 32) >= (1ll << 31)) return EFLA_ERR_UNSUPPORTED;      // strips of 32 channels
     return EFLA_OK;
 }
 
@@ -307,7 +307,7 @@ int efla_pages_free(void* pages, int n_pages, int n_slots, const int* slots, int
     size_t span;
     const int st = check_pages(pages, n_pages, n_slots, nullptr, 0, 0, &span);
     if (st != EFLA_OK) return st;
-    if (n < 0) return EFLA_ERR_INVALID_ARG;
+    if (n < 0 || n > (1 << 28)) return EFLA_ERR_INVALID_ARG;
     if (n == 0) return EFLA_OK;
     if (!slots || !aligned4(slots) ||
         overlaps(Buf{slots, (size_t)n * sizeof(int)}, Buf{pages, efla_pages_bytes(n_pages, n_slots)}))

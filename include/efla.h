@@ -418,7 +418,8 @@ int efla_backward_saved(const void *q, const void *k, const void *v, const void 
  * an empty one passes its state through.  The offsets are copied to the workspace (from pageable
  * memory that copy may synchronise the host with `stream`, and it cannot be captured; from pinned
  * memory they have to stay as they are until the call has run).
- * Supported: d up to 4096 with d * sizeof(dtype) a multiple of 16 bytes; 0 <= T <= 2^30, B, H >= 0.
+ * Supported: d up to 4096 with d * sizeof(dtype) a multiple of 16 bytes; 0 <= T <= 2^30, B, H >= 0 with
+ * B * H * ceil(d / 32) < 2^31.
  *
  * efla_scan_workspace_bytes -- workspace of efla_scan_fwd (packed != 0: with cu_seqlens), 0 for
  * arguments it would reject.  It needs no preparation.  Its first bytes hold the device error word
@@ -474,7 +475,7 @@ int efla_scan_step(const void *x, const float *g, float *S, void *o, int N, int 
  *          that are zero between calls and 2 * n_pages of any content.  efla_pages_init writes all
  *          of it; a program may read the table and owners, and write them if it keeps them
  *          consistent (page p of slot s: table[s] = p and owner[p] = s).
- * Lists of slots are int32 device arrays; an entry -1 is padding and skipped.  The calls plan on
+ * Lists of slots are int32 device arrays of at most 2^28 entries; an entry -1 is padding and skipped.  The calls plan on
  * the device: they never synchronise, can be captured and replayed, and give the same result on
  * every run.  Calls on one block have to be ordered by streams or events.
  * A wrong entry (a slot out of range; one without a page where a page is needed, or with one

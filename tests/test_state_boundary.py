@@ -156,6 +156,18 @@ def test_pages(efla):
         assert f(n=0) == OK
 
 
+def test_counts_that_would_overflow(efla):
+    """Lists and batches whose counts would pass 32 bits on the way to the device."""
+    L = efla.lib
+    assert L.efla_pages_free(P[0], 5, 7, P[1], (1 << 31) - 1, None) == INVALID
+    assert L.efla_pages_fork(P[0], 5, 7, P[1], 512, 256, P[2], P[3], (1 << 31) - 1, None) == INVALID
+    assert L.efla_pages_read(P[0], 5, 7, P[1], 1 << 20, P[2], 1 << 20, P[3], 1 << 24, None) == UNSUPPORTED
+    assert L.efla_scan_workspace_bytes(1 << 15, 1 << 15, 1, 64, 1, BF16, 0) == 0
+    assert fwd(L, B=1 << 15, H=1 << 15, T=1, S0=None, S_T=None, gw=1) == UNSUPPORTED
+    assert L.efla_scan_step(P[0], P[1], P[2], P[3], 1 << 20, 1 << 11, 64, 1, F32, 0, None) == UNSUPPORTED
+    assert L.efla_scan_workspace_bytes(1 << 15, 1 << 15, 1, 32, 1, BF16, 0) >= 1 << 37
+
+
 def test_status_names(efla):
     assert efla.efla_status_string(efla.EFLA_ERR_SLOT) == "EFLA_ERR_SLOT"
     assert efla.efla_status_string(efla.EFLA_ERR_FULL) == "EFLA_ERR_FULL"
