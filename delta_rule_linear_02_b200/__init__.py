@@ -734,6 +734,11 @@ def _pool(pool: torch.Tensor, pages: EflaPages, dtype=None) -> Tuple[int, int, i
     raise ValueError(f"pool must be [{n}, ...] with contiguous pages, got {tuple(pool.shape)}")
 
 
+def _same_device(pages: EflaPages, name: str, device) -> None:
+    if device != pages.block.device:
+        raise ValueError(f"{name} must be on {pages.block.device}, where the cache is, got {device}")
+
+
 def _slots(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None) -> Optional[int]:
     return None if t is None else _tensor(t, name, torch.int32, device, (t.numel() if n is None else n,))
 
@@ -807,6 +812,7 @@ def efla_scan_step_paged(x, g, pages: EflaPages, pool, slots, source=None, o=Non
     read from instead (-1: a zero state).  Returns o [N,H,d] (zeros for rows left out when `o` is not given)."""
     N, H, d, gw, dt = _step_shape(x, g)
     dev = x.device
+    _same_device(pages, "x", dev)
     if pool.shape[1:] != x.shape[1:]:
         raise ValueError(f"pool must be [{pages.n_pages},{H},{d}], got {tuple(pool.shape)}")
     ptr, stride, _ = _pool(pool, pages, torch.float32)
@@ -828,6 +834,7 @@ def efla_recurrent_step_paged(q, k, v, beta, pages: EflaPages, pool, slots, sour
         raise ValueError(f"k must be [N,H,d_k] and v [N,H,d_v], got {tuple(k.shape)} and {tuple(v.shape)}")
     N, H, d_k = k.shape
     d_v = v.shape[-1]
+    _same_device(pages, "k", dev)
     if pool.shape[1:] != (H, d_k, d_v):
         raise ValueError(f"pool must be [{pages.n_pages},{H},{d_k},{d_v}], got {tuple(pool.shape)}")
     ptr, stride, _ = _pool(pool, pages, torch.float32)

@@ -188,3 +188,14 @@ def test_binding_checks_its_tensors(efla):
                 lambda: efla.EflaPages(torch.zeros(100, dtype=torch.int32), 3, 4)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_binding_refuses_rows_on_another_device_than_the_cache(efla):
+    class Cache:
+        block, n_pages, n_slots = torch.empty(64, dtype=torch.int32, device="meta"), 3, 4
+
+    x, S, slots = torch.zeros(2, 3, 64), torch.zeros(3, 3, 64), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="where the cache is"):
+        efla.efla_scan_step_paged(x, x, Cache, S, slots)
+    with pytest.raises(ValueError, match="where the cache is"):
+        efla.efla_recurrent_step_paged(x, x, x, x[..., 0], Cache, torch.zeros(3, 3, 64, 64), slots)
