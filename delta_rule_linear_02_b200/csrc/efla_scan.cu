@@ -113,6 +113,7 @@ struct Stager {
         const int lane = threadIdx.x & 31, head = G.tokens * G.box, there = rows(t0) * G.box;
         for (int p = 0; p < G.heads; ++p)
             for (int i = (p < heads ? there : 0) + lane * 4; i < head; i += 128) st4(dst + p * head + i, all4(0.f));
+        fence_proxy_async_smem();      // (a later tile's copy may write there)
     }
     template <typename E>
     __device__ __forceinline__ void stage(E* dst, const E* src, const CUtensorMap* map, int t0, uint64_t* bar) const {
@@ -227,6 +228,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t in_block(uint32_t smem_addr, uint32_t rank) {

@@ -409,7 +409,9 @@ int efla_backward_saved(const void *q, const void *k, const void *v, const void 
  * g <= 0 decays), and one token is the exact flow of dh/dtau = g h + x over its unit interval,
  *     h_t = e^{g_t} h_{t-1} + phi(g_t) x_t,   o_t = h_t,   phi(g) = (e^g - 1) / g, phi(0) = 1;
  * EFLA_RULE_EULER writes with 1 in the place of phi.  g = -inf forgets everything and, under the
- * exact rule, writes nothing (phi = 0).
+ * exact rule, writes nothing (phi = 0).  g > 0 grows; the decays of up
+ * to 32 consecutive tokens are multiplied before they meet the state, so their product has to stay
+ * in float32's range too (e^88) for the result to be that of one token after the other.
  *
  *   x, o  [B,H,T,d] (dtype);  g float32, [B,H,T,d] (g_width = d) or [B,H,T] (g_width = 1: one
  *   decay for all channels of a head);  S0, S_T [B,H,d] float32.

@@ -160,6 +160,14 @@ def test_resets_and_extreme_decays(efla, cuda):
     assert float(got["o"].abs().max()) == 0 and float(got["dx"].abs().max()) == 0
 
 
+@pytest.mark.parametrize("per_channel", [True, False])
+def test_growth(efla, cuda, per_channel):
+    """g > 0: a state that grows by up to e^2 a token, e^78 in all, and its gradients."""
+    inp = inputs(1, 3, 39, 64, torch.float32, per_channel, seed=8)
+    inp["g"].uniform_(1.5, 2.0, generator=torch.Generator().manual_seed(8))
+    check(efla, inp)
+
+
 def test_non_finite_inputs_stay_in_their_channel(efla, cuda):
     inp = inputs(1, 2, 100, 64, torch.float32, True)
     clean = run_both(efla, inp)
