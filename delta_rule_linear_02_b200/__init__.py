@@ -611,7 +611,8 @@ def efla_scan_fwd(x, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspace=No
     """The per-channel gated recurrence h_t = e^g_t h_{t-1} + phi(g_t) x_t, o_t = h_t (EFLA_RULE_EULER: 1 for phi).
     x [B,H,T,d] float32 or bfloat16; g float32, x's shape or [B,H,T] (one decay per head); S0 [B,H,d] float32 or
     None.  Packed: cu_seqlens (B + 1 offsets, ints or a CPU int32 tensor) with x [H,T,d], g [H,T,d] or [H,T].
-    (A pinned tensor of offsets has to stay as it is until the call has run, and for every replay of a captured one.)
+    (Up to 255 sequences the offsets travel with the launch.  Of more, a pinned tensor has to stay as it is until the
+    call has run, and for every replay of a captured one; captured from other memory they are refused.)
     Returns (o like x, S_T [B,H,d] float32 or None)."""
     return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule)[:2]
 

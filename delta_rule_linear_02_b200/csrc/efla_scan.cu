@@ -18,6 +18,8 @@
 // Inputs are staged some turns ahead and read from memory once; tokens behind the end and
 // channels beside a head are staged as zeros, which change nothing (e^0 = 1, x = 0).  Everything
 // is folded in token order, so the results are the same bits on every run.
+#include <string.h>
+
 #include <type_traits>
 
 #include "efla_kernels.h"
@@ -52,7 +54,7 @@ __device__ __forceinline__ void st4(T* p, const P4& v) {
 constexpr int kValues = 4096, kWarps = 8, kRun = 4, kLanes4 = 128;      // values of a tile; channels x runs of a warp
 constexpr int kComputeThreads = kWarps * 32, kChainThreads = 64, kThreads = kComputeThreads + kChainThreads;
 constexpr int kCluster = 8;        // most blocks of a cluster
-constexpr int kMarks = 8;          // tiles whose marks are kept
+constexpr int kMarks = 4;          // tiles whose marks are kept
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // How streams, channels and tokens make strips and tiles: a function of the shape alone, since
@@ -130,47 +132,79 @@ struct Stager {
     }
 };
 
-// The packed sequence that holds token t: the largest n with cu[n] <= t.
-__device__ __forceinline__ int seq_of(const ScanArgs& P, int t) {
-    if (!P.cu) return 0;
-    int lo = 0, hi = P.nseq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (P.cu[mid] <= t) lo = mid;
-        else hi = mid;
+// The packed sequence that holds token t, the largest n with cu[n] <= t, by one warp: 32 offsets at a time.
+__device__ __forceinline__ int seq_of(const int* cu, int nseq, int t) {
+    int lo = 0;
+    for (long span = nseq; span > 1;) {
+        const long step = (span + 31) / 32, at = lo + (threadIdx.x & 31) * step;
+        const int below = __popc(__ballot_sync(0xffffffffu, at < lo + span && cu[at] <= t)) - 1;
+        span = min(step, span - below * step);
+        lo += (int)(below * step);
     }
     return lo;
 }
 
-// Which of a tile's tokens begin or end a sequence (bit l of word j: token 32 j + l), and whether any does.
+// Which of a tile's tokens begin or end a sequence (bit l of word j: token 32 j + l), which sequence that is,
+// and whether any does.  The warp that stages a tile finds them, and asks for the rows of state that the
+// tile will read there: looked up by the compute warps themselves they cost a packed batch a third more time.
 struct Marks {
     uint32_t first[4], last[4];
+    int seq[kLanes4];
 };
 struct MarkRing {
     Marks m[kMarks];
     uint32_t any[kMarks];
 };
+// The part of a row of states that a strip reads, towards this SM.
+struct StateRow {
+    const float* base;      // of sequence 0, or null
+    long stride;            // floats between sequences
+    int floats;
+    __device__ __forceinline__ void prefetch(int n) const {
+        if (!base) return;
+        for (int i = 0; i < floats; i += 32)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(base + n * stride + i) : "memory");
+    }
+};
 // One warp: the sequences from the one that holds t0 on, a lane each.  (A call, so that what few
 // tiles need costs the kernels no registers.)
-__device__ __noinline__ bool find_marks(const int* cu, int nseq, int n0, int T, int t0, int t1, Marks* m) {
+__device__ __noinline__ bool find_marks(const int* cu, int nseq, int T, int t0, int t1, StateRow begins, StateRow ends,
+                                        Marks* m) {
     const int lane = threadIdx.x & 31;
     uint32_t* words = m->first;                // and m->last behind it
     if (lane < 8) words[lane] = 0;
     __syncwarp();
     bool any = false;
-    for (;; n0 += 32) {
+    for (int n0 = cu ? seq_of(cu, nseq, t0) : 0;; n0 += 32) {
         const int n = n0 + lane;
         const int from = n >= nseq ? t1 : cu ? cu[n] : 0, to = n >= nseq ? t1 : cu ? cu[n + 1] : T;
-        if (from < to && from >= t0 && from < t1) atomicOr(words + ((from - t0) >> 5), 1u << ((from - t0) & 31)), any = true;
-        if (from < to && to > t0 && to <= t1) atomicOr(words + 4 + ((to - 1 - t0) >> 5), 1u << ((to - 1 - t0) & 31)), any = true;
+        if (from < to && from >= t0 && from < t1) {
+            atomicOr(words + ((from - t0) >> 5), 1u << ((from - t0) & 31));
+            m->seq[from - t0] = n;
+            begins.prefetch(n);
+            any = true;
+        }
+        if (from < to && to > t0 && to <= t1) {
+            atomicOr(words + 4 + ((to - 1 - t0) >> 5), 1u << ((to - 1 - t0) & 31));
+            m->seq[to - 1 - t0] = n;           // (the same one, if the token is its first too)
+            ends.prefetch(n);
+            any = true;
+        }
         if (__any_sync(0xffffffffu, from >= t1)) break;
     }
     return __any_sync(0xffffffffu, any);
 }
-__device__ __forceinline__ void make_marks(const ScanArgs& P, const Geo& G, int chunk, MarkRing* ring, int slot) {
-    const int t0 = chunk * G.tokens, left = P.T - t0;
-    const bool any = (P.cu || t0 == 0 || left <= G.tokens) &&
-                     find_marks(P.cu, P.cu ? P.nseq : 1, seq_of(P, t0), P.T, t0, t0 + min(G.tokens, left), ring->m + slot);
+__device__ __forceinline__ void make_marks(const ScanArgs& P, const int* cu, const Stager& S, int chunk,
+                                           const float* begins, const float* ends, MarkRing* ring, int slot) {
+    const int t0 = chunk * S.G.tokens, left = P.T - t0;
+    bool any = false;
+    if (cu || t0 == 0 || left <= S.G.tokens) {
+        const long at = (long)S.z0 * P.d + S.c0, row = P.Z * P.d;
+        const int floats = (int)min((long)(S.G.per_head > 1 ? min(S.G.width, P.d - S.c0) : S.heads * P.d), row - at);
+        any = find_marks(cu, cu ? P.nseq : 1, P.T, t0, t0 + min(S.G.tokens, left),
+                         StateRow{begins ? begins + at : nullptr, row, floats},
+                         StateRow{ends ? ends + at : nullptr, row, floats}, ring->m + slot);
+    }
     if ((threadIdx.x & 31) == 0) ring->any[slot] = any;
 }
 __device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
@@ -178,10 +212,10 @@ __device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
 }
 
 // Sequences without tokens pass their states through.
-__device__ __forceinline__ void pass_empty(const ScanArgs& P, const float* in, float* out) {
-    if (!P.cu || !out) return;
+__device__ __forceinline__ void pass_empty(const ScanArgs& P, const int* cu, const float* in, float* out) {
+    if (!cu || !out) return;
     for (int n = blockIdx.x; n < P.nseq; n += gridDim.x)
-        if (P.cu[n] == P.cu[n + 1])
+        if (cu[n] == cu[n + 1])
             for (long i = threadIdx.x; i < P.Z * P.d; i += kThreads)
                 out[n * P.Z * P.d + i] = in ? in[n * P.Z * P.d + i] : 0.f;
 }
@@ -350,6 +384,10 @@ __device__ __forceinline__ void sum_tokens(const float* sum, float* to, int span
 struct Maps {
     CUtensorMap x, g, dO;
 };
+// The offsets of a packed batch of few sequences, as an argument.
+struct Offsets {
+    int cu[kScanInline + 1];
+};
 
 template <typename Tin, bool kShared>
 struct FwdSmem {
@@ -363,7 +401,7 @@ struct FwdSmem {
 
 template <typename Tin, bool kShared>
 __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const __grid_constant__ Maps maps, Geo G,
-                                                               int blocks) {
+                                                               int blocks, const __grid_constant__ Offsets offsets) {
     using M = FwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
     float* runs = reinterpret_cast<float*>(smem + M::kStages * M::kStage);     // [A, B (then: entering)][run][width]
@@ -376,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blocks > 1 ? (int)cluster_rank() : 0;
     const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
+    const int* cu = P.by_value ? offsets.cu : P.cu;
     if (threadIdx.x == 0) {
         if (P.clear_err && blockIdx.x == 0) *P.err = kDevOk;
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
@@ -394,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         const int t0 = chunk * G.tokens;
         Tin* dx = reinterpret_cast<Tin*>(smem + st * M::kStage);
         float* dg = reinterpret_cast<float*>(smem + st * M::kStage + M::kX);
-        make_marks(P, G, chunk, ring, n % kMarks);
+        make_marks(P, cu, stager, chunk, P.S0, nullptr, ring, n % kMarks);
         stager.zero_rest(dx, t0);
         if (!kShared) stager.zero_rest(dg, t0);
         __syncwarp();
@@ -405,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
-    pass_empty(P, P.S0, P.S_T);
+    pass_empty(P, cu, P.S0, P.S_T);
     if (blocks > 1) cluster_sync();       // every block's barriers are set up
     bool dead = false;
 
@@ -462,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                 constexpr bool plain = decltype(plain_)::value;
                 const int rule = decltype(rule_)::value < 0 ? P.rule : decltype(rule_)::value;
                 const uint32_t first = plain ? 0u : run_bits(ring->m[n % kMarks].first, L.run);
+                const int* seqs = ring->m[n % kMarks].seq + L.run * kRun;
                 // 1. the run's tokens as h = a h' + b, and the run's (A, B)
                 Gate<kShared> a;
                 P4 b[kRun], ra = all4(1.f), rb = all4(0.f);
@@ -472,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                     b[i] = mul4(w, ld4(xs + i * L.row));
                     if (!plain && (first >> i & 1u)) {       // a sequence begins: its own state enters, no other
                         if (P.S0 && L.on)
-                            b[i] = fma4(a1, ld4(P.S0 + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c), b[i]);
+                            b[i] = fma4(a1, ld4(P.S0 + ((long)seqs[i] * P.Z + L.z) * P.d + L.c), b[i]);
                         a1 = all4(0.f);
                     }
                     a.set(i, a1);
@@ -498,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                     h = fma4(a.at(i), h, b[i]);
                     if (P.o && i < live) st4(out + i * P.d, h);
                     if (!plain && (last >> i & 1u) && L.on)
-                        st4(P.S_T + ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c, h);
+                        st4(P.S_T + ((long)seqs[i] * P.Z + L.z) * P.d + L.c, h);
                 }
             };
             if (ring->any[n % kMarks]) tile(std::false_type(), std::integral_constant<int, -1>());
@@ -528,7 +568,7 @@ struct BwdSmem {
 
 template <typename Tin, bool kShared>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const __grid_constant__ Maps maps, Geo G,
-                                                               int blocks) {
+                                                               int blocks, const __grid_constant__ Offsets offsets) {
     using M = BwdSmem<Tin, kShared>;
     extern __shared__ __align__(128) char smem[];
     // [A, B (then: the state entering), reverse A, R (then: the flow entering)][run][width]
@@ -544,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blocks > 1 ? (int)cluster_rank() : 0;
     const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
+    const int* cu = P.by_value ? offsets.cu : P.cu;
     if (threadIdx.x == 0) {
         if (P.clear_err && blockIdx.x == 0) *P.err = kDevOk;
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1), mbar_init(spent + i, kWarps);
@@ -562,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
         const int t0 = chunk * G.tokens;
         Tin* sx = reinterpret_cast<Tin*>(smem + st * M::kStage);
         float* sg = reinterpret_cast<float*>(smem + st * M::kStage + 2 * M::kX);
-        make_marks(P, G, chunk, ring, n % kMarks);
+        make_marks(P, cu, stager, chunk, P.S0, P.dST, ring, n % kMarks);
         stager.zero_rest(sx, t0);
         stager.zero_rest(sx + kValues, t0);
         if (!kShared) stager.zero_rest(sg, t0);
@@ -575,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     };
     if (warp == kThreads / 32 - 1)
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
-    pass_empty(P, P.dST, P.dS0);
+    pass_empty(P, cu, P.dST, P.dS0);
     if (blocks > 1) cluster_sync();
     bool dead = false;
 
@@ -651,7 +692,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
                 const int rule = decltype(rule_)::value < 0 ? P.rule : decltype(rule_)::value;
                 const uint32_t first = plain ? 0u : run_bits(ring->m[n % kMarks].first, L.run);
                 const uint32_t last = plain ? 0u : run_bits(ring->m[n % kMarks].last, L.run);
-                auto row_of = [&](int i) { return ((long)seq_of(P, tw + i) * P.Z + L.z) * P.d + L.c; };
+                // (volatile: read where it is needed, and not held in registers that the products want)
+                auto row_of = [&](int i) {
+                    const int seq = *const_cast<volatile int*>(&ring->m[n % kMarks].seq[L.run * kRun + i]);
+                    return ((long)seq * P.Z + L.z) * P.d + L.c;
+                };
                 auto row = [&](const float* from, int i) { return from && L.on ? ld4(from + row_of(i)) : all4(0.f); };
                 // 1. the gates, and the run's (A, B) forward and in reverse
                 Gate<kShared> a, w, dw;
@@ -907,11 +952,13 @@ cudaError_t launch_clusters(Kernel kernel, int (*smem)(int), Room* rooms, const 
         (!map_tokens<Tin>(&maps.x, a.x, a, G) || (!kShared && !map_tokens<float>(&maps.g, a.g, a, G)) ||
          (a.dO && !map_tokens<Tin>(&maps.dO, a.dO, a, G))))
         return cudaErrorInvalidValue;
+    Offsets offsets;
+    if (a.by_value) memcpy(offsets.cu, a.cu, ((size_t)a.nseq + 1) * sizeof(int));
     const int blocks = pick_blocks(room, G);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     config(kernel, blocks, smem(blocks), G.strips, stream, &cfg, attr);
-    return cudaLaunchKernelEx(&cfg, kernel, a, maps, G, blocks);
+    return cudaLaunchKernelEx(&cfg, kernel, a, maps, G, blocks, offsets);
 }
 
 template <typename Tin, bool kShared>

@@ -54,6 +54,23 @@ bool good_offsets(const int* cu, int N, int T) {
     return true;
 }
 
+// Where a call's kernels find the offsets: in its launches' arguments, or copied to `to`.  A captured copy would
+// read the host array again on every replay, so it is refused from memory that is not pinned.
+int place_offsets(const int* cu, int B, bool copy, char* to, cudaStream_t s, efla::ScanArgs* a) {
+    a->by_value = B <= efla::kScanInline;
+    a->cu = a->by_value ? cu : reinterpret_cast<const int*>(to);
+    if (a->by_value || !copy) return EFLA_OK;
+    cudaStreamCaptureStatus capture;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return EFLA_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) {
+        cudaPointerAttributes at;
+        if (cudaPointerGetAttributes(&at, cu) != cudaSuccess) return EFLA_ERR_CUDA;
+        if (at.type != cudaMemoryTypeHost) return EFLA_ERR_INVALID_ARG;
+    }
+    return cudaMemcpyAsync(to, cu, ((size_t)B + 1) * sizeof(int), cudaMemcpyHostToDevice, s) == cudaSuccess ? EFLA_OK
+                                                                                                           : EFLA_ERR_CUDA;
+}
+
 size_t cu_bytes(int B, bool packed) { return packed ? (((size_t)B + 1) * sizeof(int) + 255) & ~(size_t)255 : 0; }
 
 }  // namespace
@@ -100,13 +117,11 @@ int efla_scan_fwd(const void* x, const float* g, const int* cu_seqlens, const fl
     }
     if (!x || !g || !o || !aligned16(x) || !aligned16(g) || !aligned16(o)) return EFLA_ERR_INVALID_ARG;
     char* ws = static_cast<char*>(workspace);
-    if (packed && cudaMemcpyAsync(ws + kHeader, cu_seqlens, ((size_t)B + 1) * sizeof(int), cudaMemcpyHostToDevice, s) !=
-                      cudaSuccess)
-        return EFLA_ERR_CUDA;
     efla::ScanArgs a;
+    const int placed = packed ? place_offsets(cu_seqlens, B, true, ws + kHeader, s, &a) : EFLA_OK;
+    if (placed != EFLA_OK) return placed;
     a.x = x;
     a.g = g;
-    a.cu = packed ? reinterpret_cast<const int*>(ws + kHeader) : nullptr;
     a.nseq = packed ? B : 1;
     a.Z = Z;
     a.T = T;
@@ -156,14 +171,12 @@ int efla_scan_backward(const void* x, const float* g, const int* cu_seqlens, con
     char* ws = static_cast<char*>(workspace);
     const bool bf16 = dtype == EFLA_DTYPE_BF16;
     // without saved states the workspace holds a forward's in front of the backward's
-    const char* states = saved ? static_cast<const char*>(saved) : ws;
-    if (!saved && packed && cudaMemcpyAsync(ws + kHeader, cu_seqlens, ((size_t)B + 1) * sizeof(int),
-                                            cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return EFLA_ERR_CUDA;
+    char* states = saved ? static_cast<char*>(const_cast<void*>(saved)) : ws;
     efla::ScanArgs a;
+    const int placed = packed ? place_offsets(cu_seqlens, B, !saved, states + kHeader, s, &a) : EFLA_OK;
+    if (placed != EFLA_OK) return placed;
     a.x = x;
     a.g = g;
-    a.cu = packed ? reinterpret_cast<const int*>(states + kHeader) : nullptr;
     a.nseq = packed ? B : 1;
     a.Z = Z;
     a.T = T;
@@ -171,7 +184,7 @@ int efla_scan_backward(const void* x, const float* g, const int* cu_seqlens, con
     a.gw = g_width;
     a.rule = rule;
     a.S0 = S0;
-    a.E = const_cast<float*>(reinterpret_cast<const float*>(states + kHeader + cu_bytes(B, packed)));
+    a.E = reinterpret_cast<float*>(states + kHeader + cu_bytes(B, packed));
     a.err = reinterpret_cast<uint32_t*>(ws);
     if (!saved) {   // the states alone: a forward without outputs
         a.scratch = ws + kHeader + cu_bytes(B, packed) + efla::scan_states_bytes(Z, T, d);

@@ -417,9 +417,11 @@ int efla_backward_saved(const void *q, const void *k, const void *v, const void 
  *   decay for all channels of a head);  S0, S_T [B,H,d] float32.
  * Packed batches: with cu_seqlens (a HOST array of B + 1 offsets as in efla_chunk_fwd_varlen, T =
  * cu_seqlens[B]) the tensors are [H,T,d], [H,T,(d)] and every sequence runs from its own S0 row;
- * an empty one passes its state through.  The offsets are copied to the workspace (from pageable
- * memory that copy may synchronise the host with `stream`, and it cannot be captured; from pinned
- * memory they have to stay as they are until the call has run).
+ * an empty one passes its state through.  The offsets of up to 255 sequences travel with the launch:
+ * the array is free when the call returns, and a captured call holds its own copy.  Those of more are
+ * copied to the workspace (from pageable memory that copy may synchronise the host with `stream`, and a
+ * call that is being captured refuses it with EFLA_ERR_INVALID_ARG; pinned memory has to stay as it is
+ * until the call has run, and for every replay of a captured one).
  * Supported: d up to 4096 with d * sizeof(dtype) a multiple of 16 bytes; 0 <= T <= 2^30, B, H >= 0 with
  * B * H * ceil(d / 32) < 2^31.
  *
@@ -472,7 +474,7 @@ int efla_scan_step(const void *x, const float *g, float *S, void *o, int N, int 
  *          of 16).  A call works on data_bytes of each page from `pool` on, so that a page may
  *          hold several layers and a step is given the pool at its layer's offset.
  *   pages  the block, efla_pages_bytes(n_pages, n_slots) bytes, 16-byte aligned, in int32 words:
- *          64 of header (word 0: errors, the others zero between calls), n_slots of table (slot ->
+ *          64 of header (word 0: errors, word 1 of any content, the others zero between calls), n_slots of table (slot ->
  *          page, -1: none), n_pages of owners (page -> slot, -1: free), then scratch: n_slots words
  *          that are zero between calls and 2 * n_pages of any content.  efla_pages_init writes all
  *          of it; a program may read the table and owners, and write them if it keeps them

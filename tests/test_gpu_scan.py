@@ -115,6 +115,58 @@ def test_packed(efla, cuda, lengths, per_channel, dtype):
             assert torch.equal(got["dS0"][n].cpu(), inp["dS_T"][n])
 
 
+@pytest.mark.parametrize("per_channel", [True, False])
+def test_packed_many_sequences(efla, cuda, per_channel):
+    """More sequences than a launch carries the offsets of, most of them short or empty, many in one tile."""
+    lengths = [(7 * i) % 11 if i % 3 else 0 for i in range(400)] + [0] * 50 + [300]
+    cu = offsets(lengths)
+    inp = inputs(len(lengths), 2, cu[-1], 64, torch.bfloat16, per_channel, cu=cu, seed=12)
+    got = check(efla, inp, cu)
+    again = run_both(efla, inp, cu, saved=False)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("count", [255, 256])
+def test_captured_packed_batch(efla, cuda, count):
+    """A captured call replayed after its list is gone; offsets that it would have to copy from there are refused."""
+    lengths = [(5 * i) % 7 for i in range(count)]
+    cu = offsets(lengths)
+    inp = inputs(count, 2, cu[-1], 64, torch.float32, True, cu=cu, seed=13)
+    want, t = run_both(efla, inp, cu), dev(inp)
+    graph = torch.cuda.CUDAGraph()
+
+    def train(cu):
+        o, S_T, saved = efla.efla_scan_fwd_save(t["x"], t["g"], S0=t["S0"], cu_seqlens=cu)
+        dx, dg, dS0 = efla.efla_scan_backward(t["x"], t["g"], t["dO"], S0=t["S0"], dS_T=t["dS_T"], saved=saved,
+                                              cu_seqlens=cu)
+        return dict(o=o, S_T=S_T, dx=dx, dg=dg, dS0=dS0)
+
+    if count > 255:
+        with pytest.raises(efla.EflaError) as refused, torch.cuda.graph(graph):
+            train(list(cu))
+        assert refused.value.status == efla.EFLA_ERR_INVALID_ARG
+        graph = torch.cuda.CUDAGraph()
+    pinned = torch.tensor(cu, dtype=torch.int32).pin_memory()
+    with torch.cuda.graph(graph):
+        out = train(list(cu) if count <= 255 else pinned)
+    for _ in range(2):
+        for v in out.values():
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], want[k]) for k in want)
+
+
+def test_change_of_formula(efla, cuda):
+    """Decays on both sides of |g| = 1, where the gates change their formula, and next to it."""
+    inp = inputs(1, 2, 160, 64, torch.float32, True, seed=6)
+    edge = torch.tensor([1.0, 1.0 - 2.0 ** -24, 1.0 + 2.0 ** -23, 0.9999, 1.0001, 0.5, 2.0, 1e-7])
+    inp["g"] = -edge[torch.randint(0, len(edge), inp["g"].shape, generator=torch.Generator().manual_seed(6))]
+    check(efla, inp)
+    inp["g"][:, :, ::2] *= -1           # growth and decay in turn
+    check(efla, inp)
+
+
 def test_packed_without_states(efla, cuda):
     cu = offsets(MIX)
     check(efla, inputs(len(MIX), 2, cu[-1], 128, torch.bfloat16, True, cu=cu, state=False), cu, rule=EULER)
