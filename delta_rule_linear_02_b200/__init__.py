@@ -1,6 +1,6 @@
 """Python binding of libefla.so, the B200 Exact Flow Linear Attention forward.
 
-Argument marshalling only: every step of the computation runs in the library's CUDA
+Argument checks and marshalling only: every step of the computation runs in the library's CUDA
 kernels.  PyTorch provides device memory and streams.  The names mirror the C ABI of
 include/efla.h.  Importing this package loads the in-tree libefla.so and fails loudly if
 it has not been built (python delta_rule_linear_02_b200/build.py).
@@ -35,10 +35,16 @@ class EflaError(RuntimeError):
         super().__init__(f"{where}: {efla_status_string(status)} ({status})")
 
 
+_native = None      # the short way of the calls whose time is the call itself (csrc/efla_native.cpp)
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
+    global _native
     if not os.path.exists(path):
         raise ImportError(f"{os.path.basename(path)} is not built at {path}; run "
                           "`python delta_rule_linear_02_b200/build.py` (nvcc, sm_100a)")
+    if _native is None:
+        from . import _efla_native as _native
     lib = ctypes.CDLL(path)
     vp, I, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_size_t
     lib.efla_status_string.argtypes = [I]
@@ -118,6 +124,11 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     for f in (lib.efla_pages_init, lib.efla_pages_free, lib.efla_pages_compact, lib.efla_pages_status,
               lib.efla_pages_fork, lib.efla_pages_copy, lib.efla_pages_write, lib.efla_pages_read):
         f.restype = I
+    # their order is that of Entries in csrc/efla_native.cpp
+    lib.entries = _native.bind(*(ctypes.cast(f, vp).value for f in (
+        lib.efla_scan_workspace_bytes, lib.efla_scan_fwd, lib.efla_scan_backward_workspace_bytes, lib.efla_scan_backward,
+        lib.efla_scan_step, lib.efla_scan_step_paged, lib.efla_recurrent_step_paged, lib.efla_pages_fork,
+        lib.efla_pages_copy, lib.efla_pages_free, lib.efla_pages_compact)))
     return lib
 
 
@@ -514,6 +525,15 @@ def _call(fn, where: str, device: torch.device, stream, *args):
         raise EflaError(status, where)
 
 
+def _made(out, where: str) -> bool:
+    """Whether the native way has made the call (None: it is for the way below); raises what the library answered."""
+    if out is None:
+        return False
+    if type(out) is int and out != EFLA_OK:
+        raise EflaError(out, where)
+    return True
+
+
 def _made_here(stream, *tensors) -> None:
     """Tensors that a call allocated itself and uses on `stream`: their memory is not given away before it has run."""
     if stream is not None:
@@ -573,6 +593,10 @@ def efla_scan_workspace_bytes(B, H, T, d, g_width, dtype=torch.bfloat16, packed:
 
 
 def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule):
+    if stream is None:
+        out = _native.scan_fwd(lib.entries, x, g, S0, cu_seqlens, o, S_T, workspace, want_state, rule)
+        if _made(out, "efla_scan_fwd"):
+            return out
     B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
     dev, f32 = x.device, torch.float32
     if dev.index is None:
@@ -629,6 +653,10 @@ def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None
     """Gradients of efla_scan_fwd for the loss sum(dO * o) + sum(dS_T * S_T): (dx, dg, dS0 or None), all float32.
     dO like x, dS_T [B,H,d] float32 or None; saved: from efla_scan_fwd_save on the same x, g, S0, cu_seqlens and rule
     (None: computed again).  `grads` may supply the three tensors preallocated (dS0 may be None)."""
+    if stream is None and grads is None and workspace is None:
+        out = _native.scan_backward(lib.entries, x, g, dO, S0, dS_T, saved, cu_seqlens, want_dS0, rule)
+        if _made(out, "efla_scan_backward"):
+            return out
     B, H, T, d, gw, dt, cu = _scan_shape(x, g, cu_seqlens)
     dev, f32 = x.device, torch.float32
     px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", f32, dev, g.shape)
@@ -669,6 +697,10 @@ def _step_shape(x: torch.Tensor, g: torch.Tensor):
 def efla_scan_step(x, g, S, o=None, stream=None, rule: int = EFLA_RULE_EXACT) -> torch.Tensor:
     """One token of efla_scan_fwd's recurrence: x [N,H,d], g float32 [N,H,d] or [N,H]; S [N,H,d] float32 updated in
     place.  Returns o [N,H,d]."""
+    if stream is None:
+        out = _native.scan_step(lib.entries, x, g, S, o, rule)
+        if _made(out, "efla_scan_step"):
+            return out
     N, H, d, gw, dt = _step_shape(x, g)
     dev = x.device
     if o is None:
@@ -748,6 +780,9 @@ def _slots(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None
 def efla_pages_fork(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Tensor, stream=None) -> None:
     """Every empty slot dest[i] gets a free page with a copy of slot source[i]'s page (-1: zeros).  pool [n_pages, ...]
     (any type), or None: pages are given without copying.  source, dest: int32, -1 in dest is padding."""
+    if stream is None and _made(_native.pages_fork(lib.entries, pages.block, pages.n_pages, pages.n_slots, pool, source,
+                                               dest), "efla_pages_fork"):
+        return
     dev = pages.block.device
     ptr, stride, data = (None, 0, 0) if pool is None else _pool(pool, pages)
     _call(lib.efla_pages_fork, "efla_pages_fork", dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr,
@@ -756,6 +791,9 @@ def efla_pages_fork(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Te
 
 def efla_pages_copy(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Tensor, stream=None) -> None:
     """Slot dest[i]'s page becomes a copy of slot source[i]'s (-1: zeros), all entries as if at once."""
+    if stream is None and _made(_native.pages_copy(lib.entries, pages.block, pages.n_pages, pages.n_slots, pool, source,
+                                               dest), "efla_pages_copy"):
+        return
     dev = pages.block.device
     ptr, stride, data = _pool(pool, pages)
     _call(lib.efla_pages_copy, "efla_pages_copy", dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots, ptr,
@@ -764,6 +802,9 @@ def efla_pages_copy(pages: EflaPages, pool, source: torch.Tensor, dest: torch.Te
 
 def efla_pages_free(pages: EflaPages, slots: torch.Tensor, stream=None) -> None:
     """The slots' pages are free again and the slots empty."""
+    if stream is None and _made(_native.pages_free(lib.entries, pages.block, pages.n_pages, pages.n_slots, slots),
+                                "efla_pages_free"):
+        return
     dev = pages.block.device
     _call(lib.efla_pages_free, "efla_pages_free", dev, stream, pages.block.data_ptr(), pages.n_pages, pages.n_slots,
           _slots(slots, "slots", dev), slots.numel())
@@ -771,6 +812,9 @@ def efla_pages_free(pages: EflaPages, slots: torch.Tensor, stream=None) -> None:
 
 def efla_pages_compact(pages: EflaPages, pool, stream=None) -> None:
     """Moves pages so that the ones in use are the pool's first."""
+    if stream is None and _made(_native.pages_compact(lib.entries, pages.block, pages.n_pages, pages.n_slots, pool),
+                                "efla_pages_compact"):
+        return
     ptr, stride, data = _pool(pool, pages)
     _call(lib.efla_pages_compact, "efla_pages_compact", pages.block.device, stream, pages.block.data_ptr(),
           pages.n_pages, pages.n_slots, ptr, stride, data)
@@ -812,6 +856,11 @@ def efla_scan_step_paged(x, g, pages: EflaPages, pool, slots, source=None, o=Non
     """efla_scan_step on a state cache: row n's state is the page of slot slots[n] in pool [n_pages,H,d] float32.
     slots [N] int32, -1: a padded row, whose o is left as it was; source [N] int32: the slot a row's entering state is
     read from instead (-1: a zero state).  Returns o [N,H,d] (zeros for rows left out when `o` is not given)."""
+    if stream is None:
+        out = _native.scan_step_paged(lib.entries, x, g, pages.block, pages.n_pages, pages.n_slots, pool, slots, source, o,
+                                      rule)
+        if _made(out, "efla_scan_step_paged"):
+            return out
     N, H, d, gw, dt = _step_shape(x, g)
     dev = x.device
     _same_device(pages, "x", dev)
@@ -831,6 +880,11 @@ def efla_recurrent_step_paged(q, k, v, beta, pages: EflaPages, pool, slots, sour
                               rule: int = EFLA_RULE_EXACT) -> torch.Tensor:
     """efla_recurrent_step (with g [N,H] float32: efla_recurrent_step_gated) on a state cache: row n's state is the
     page of slot slots[n] in pool [n_pages,H,d_k,d_v] float32.  slots, source and o as in efla_scan_step_paged."""
+    if stream is None:
+        out = _native.recurrent_step_paged(lib.entries, q, k, v, beta, pages.block, pages.n_pages, pages.n_slots, pool,
+                                           slots, source, g, o, rule)
+        if _made(out, "efla_recurrent_step_paged"):
+            return out
     dt, dev = k.dtype, k.device
     if k.dim() != 3 or v.dim() != 3:
         raise ValueError(f"k must be [N,H,d_k] and v [N,H,d_v], got {tuple(k.shape)} and {tuple(v.shape)}")
