@@ -19,14 +19,15 @@ constexpr int kCols = 32;
 constexpr int kThreads = 256;
 
 template <typename Tin, int D>
-__global__ void __launch_bounds__(kThreads) decode_paged_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k,
-                                                                const Tin* __restrict__ v,
-                                                                const Tin* __restrict__ beta,
-                                                                const float* __restrict__ g, char* pool,
-                                                                Tin* __restrict__ o, int N, int H, int rule,
+__global__ void __launch_bounds__(kThreads) decode_paged_kernel(const Tin* q, const Tin* k,
+                                                                const Tin* v,
+                                                                const Tin* beta,
+                                                                const float* g, char* pool,
+                                                                Tin* o, int N, int H, int rule,
                                                                 PagedRows P) {
     constexpr int RPT = D / 32;
     constexpr int SLICES = D / kCols;
+    after_previous();
     const int t = threadIdx.x, cq = t & 7, rg = t >> 3, warp = t >> 5, lane = t & 31;
     const long head = blockIdx.x / SLICES;
     const int n = (int)(head / H), hh = (int)(head % H);
@@ -159,11 +160,11 @@ __device__ __forceinline__ RowPages paged_row_warp(const PagedRows& P, int N, in
 }
 
 template <typename Tin, int D>
-__global__ void __launch_bounds__(kStreamThreads, 1) decode_stream_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k,
-                                                                          const Tin* __restrict__ v,
-                                                                          const Tin* __restrict__ beta,
-                                                                          const float* __restrict__ g, char* pool,
-                                                                          Tin* __restrict__ o, int N, int H, int rule,
+__global__ void __launch_bounds__(kStreamThreads, 1) decode_stream_kernel(const Tin* q, const Tin* k,
+                                                                          const Tin* v,
+                                                                          const Tin* beta,
+                                                                          const float* g, char* pool,
+                                                                          Tin* o, int N, int H, int rule,
                                                                           PagedRows P) {
     using M = StreamSmem<Tin, D>;
     extern __shared__ __align__(128) char smem[];
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) decode_stream_kernel(const 
         fence_mbar_init();
     }
     __syncthreads();
+    after_previous();
 
     if (warp == kWorkers / 32) {          // the producer
         const int per_row = (H + M::kHeads - 1) / M::kHeads;
@@ -358,16 +360,14 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const void* be
     if (jobs >= (D == 64 ? 1 : 3) * sms) {
         static std::atomic<uint64_t> limit{0};
         if ((e = set_smem_limit_once(decode_stream_kernel<Tin, D>, M::kBytes, limit)) != cudaSuccess) return e;
-        decode_stream_kernel<Tin, D><<<sms, kStreamThreads, M::kBytes, stream>>>(
-            (const Tin*)q, (const Tin*)k, (const Tin*)v, (const Tin*)beta, g, reinterpret_cast<char*>(pool), (Tin*)o, N, H,
-            rule, paged);
-        return cudaGetLastError();
+        return launch_after(decode_stream_kernel<Tin, D>, sms, kStreamThreads, M::kBytes, stream, (const Tin*)q,
+                            (const Tin*)k, (const Tin*)v, (const Tin*)beta, g, reinterpret_cast<char*>(pool),
+                            (Tin*)o, N, H, rule, paged);
     }
     const long blocks = (long)N * H * (D / kCols);
-    decode_paged_kernel<Tin, D><<<(unsigned)blocks, kThreads, 0, stream>>>(
-        (const Tin*)q, (const Tin*)k, (const Tin*)v, (const Tin*)beta, g, reinterpret_cast<char*>(pool), (Tin*)o, N, H,
-        rule, paged);
-    return cudaGetLastError();
+    return launch_after(decode_paged_kernel<Tin, D>, (unsigned)blocks, kThreads, 0, stream, (const Tin*)q,
+                        (const Tin*)k, (const Tin*)v, (const Tin*)beta, g, reinterpret_cast<char*>(pool), (Tin*)o, N,
+                        H, rule, paged);
 }
 }  // namespace
 

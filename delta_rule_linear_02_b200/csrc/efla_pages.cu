@@ -41,6 +41,7 @@ __device__ __forceinline__ int block_rank(bool flag, int* total) {
 }
 
 __global__ void pages_init_kernel(PagesBlock b) {
+    after_previous();
     const int words = b.n_slots + b.n_pages;
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < kPagesHeader) reinterpret_cast<int*>(b.err)[i] = 0;
@@ -48,7 +49,8 @@ __global__ void pages_init_kernel(PagesBlock b) {
     if (i < b.n_slots + 2 * b.n_pages) b.claim[i] = 0;           // claims and the move list too
 }
 
-__global__ void pages_free_kernel(PagesBlock b, const int* __restrict__ slots, int n) {
+__global__ void pages_free_kernel(PagesBlock b, const int* slots, int n) {
+    after_previous();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
     const int s = slots[i];
@@ -101,6 +103,7 @@ __device__ __forceinline__ bool plan_entry(const PagesBlock& b, const int* sourc
 
 __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan(PagesBlock b, const int* source, const int* dest,
                                                                 int n) {
+    after_previous();
     claim_slots(b, dest, n);
     int count = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
@@ -140,6 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan(PagesBlock b, co
 
 __global__ void __launch_bounds__(kPlanThreads) pages_copy_plan(PagesBlock b, const int* source, const int* dest,
                                                                 int n) {
+    after_previous();
     claim_slots(b, dest, n);
     int count = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
@@ -159,6 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_copy_plan(PagesBlock b, co
 }
 
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan(PagesBlock b) {
+    after_previous();
     int live = 0;
     for (int base = 0; base < b.n_pages; base += kPlanThreads) {
         const int p = base + threadIdx.x;
@@ -220,6 +225,7 @@ __device__ __forceinline__ void move_pages(const int* src, const int* dst, int m
 }
 
 __global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs) {
+    after_previous();
     move_pages(b.src, b.dst, *b.moves, pool, page_bytes, vecs);
 }
 
@@ -285,10 +291,11 @@ __device__ __forceinline__ bool last_block(const PagesBlock& b) {
     return last;
 }
 
-__global__ void __launch_bounds__(kMoveThreads) pages_fork_kernel(PagesBlock b, const int* __restrict__ source,
-                                                                  const int* __restrict__ dest, int n, char* pool,
+__global__ void __launch_bounds__(kMoveThreads) pages_fork_kernel(PagesBlock b, const int* source,
+                                                                  const int* dest, int n, char* pool,
                                                                   size_t page_bytes, long vecs) {
     __shared__ FusedPlan plan;
+    after_previous();
     const int i = threadIdx.x, to = i < n ? dest[i] : -1, from = i < n ? source[i] : -1;
     // the free pages of this thread's stretch
     const int per = (b.n_pages + kMoveThreads - 1) / kMoveThreads, p0 = i * per;
@@ -320,6 +327,7 @@ __global__ void __launch_bounds__(kMoveThreads) pages_fork_kernel(PagesBlock b, 
 
 __global__ void __launch_bounds__(kMoveThreads) pages_compact_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs) {
     __shared__ FusedPlan plan;
+    after_previous();
     const int per = (b.n_pages + kMoveThreads - 1) / kMoveThreads, p0 = threadIdx.x * per;
     uint32_t used = 0;
 #pragma unroll
@@ -367,14 +375,16 @@ __device__ __forceinline__ void move_strip(const int* src, const int* dst, int m
 __global__ void __launch_bounds__(kMoveThreads) pages_strip_kernel(PagesBlock b, char* pool, size_t page_bytes, long vecs,
                                                                    int width) {
     extern __shared__ uint4 held[];
+    after_previous();
     move_strip(b.src, b.dst, *b.moves, pool, page_bytes, vecs, width, held);
 }
 
-__global__ void __launch_bounds__(kMoveThreads) pages_copy_kernel(PagesBlock b, const int* __restrict__ source,
-                                                                  const int* __restrict__ dest, int n, char* pool,
+__global__ void __launch_bounds__(kMoveThreads) pages_copy_kernel(PagesBlock b, const int* source,
+                                                                  const int* dest, int n, char* pool,
                                                                   size_t page_bytes, long vecs, int width) {
     extern __shared__ uint4 held[];
     __shared__ int dests[kFusedList], src[kFusedList], dst[kFusedList];
+    after_previous();
     const int i = threadIdx.x, to = i < n ? dest[i] : -1, from = i < n ? source[i] : -1;
     dests[i] = to;
     __syncthreads();
@@ -392,8 +402,9 @@ __global__ void __launch_bounds__(kMoveThreads) pages_copy_kernel(PagesBlock b, 
 
 // Rows into the pages of their slots (write) or out of them; one block per 4 KiB of a row.
 __global__ void __launch_bounds__(256) pages_rows_kernel(PagesBlock b, char* pool, size_t page_bytes, char* rows,
-                                                         size_t row_bytes, const int* __restrict__ slots, int n,
+                                                         size_t row_bytes, const int* slots, int n,
                                                          int pieces, bool write) {
+    after_previous();
     const int i = blockIdx.x / pieces;
     const size_t at = ((size_t)(blockIdx.x % pieces) * 256 + threadIdx.x) * 16;
     const int s = slots[i];
@@ -424,22 +435,17 @@ int move_grid() {
 
 cudaError_t launch_pages_init(const PagesBlock& b, cudaStream_t stream) {
     const int words = b.n_slots + 2 * b.n_pages + kPagesHeader;
-    pages_init_kernel<<<(words + 255) / 256, 256, 0, stream>>>(b);
-    return cudaGetLastError();
+    return launch_after(pages_init_kernel, (words + 255) / 256, 256, 0, stream, b);
 }
 
 cudaError_t launch_pages_free(const PagesBlock& b, const int* slots, int n, cudaStream_t stream) {
-    pages_free_kernel<<<(n + 255) / 256, 256, 0, stream>>>(b, slots, n);
-    return cudaGetLastError();
+    return launch_after(pages_free_kernel, (n + 255) / 256, 256, 0, stream, b, slots, n);
 }
 
 static cudaError_t launch_moves(const PagesBlock& b, void* pool, size_t page_bytes, size_t data_bytes,
                                 cudaStream_t stream) {
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    pages_move_kernel<<<move_grid(), kMoveThreads, 0, stream>>>(b, static_cast<char*>(pool), page_bytes,
-                                                                (long)(data_bytes / 16));
-    return cudaGetLastError();
+    return launch_after(pages_move_kernel, move_grid(), kMoveThreads, 0, stream, b, static_cast<char*>(pool),
+                        page_bytes, (long)(data_bytes / 16));
 }
 
 // A fused call's blocks: what its largest possible number of moves keeps busy.
@@ -452,12 +458,11 @@ cudaError_t launch_pages_fork(const PagesBlock& b, void* pool, size_t page_bytes
                               const int* dest, int n, cudaStream_t stream) {
     const long vecs = pool ? (long)(data_bytes / 16) : 0;
     if (n <= kFusedList && b.n_pages <= kFusedPages) {
-        pages_fork_kernel<<<fused_grid(n, vecs), kMoveThreads, 0, stream>>>(b, source, dest, n, static_cast<char*>(pool),
-                                                                            page_bytes, vecs);
-        return cudaGetLastError();
+        return launch_after(pages_fork_kernel, fused_grid(n, vecs), kMoveThreads, 0, stream, b, source, dest, n,
+                            static_cast<char*>(pool), page_bytes, vecs);
     }
-    pages_fork_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
-    if (!pool) return cudaGetLastError();
+    const cudaError_t e = launch_after(pages_fork_plan, 1, kPlanThreads, 0, stream, b, source, dest, n);
+    if (e != cudaSuccess || !pool) return e;
     return launch_moves(b, pool, page_bytes, data_bytes, stream);
 }
 
@@ -465,11 +470,11 @@ cudaError_t launch_pages_compact(const PagesBlock& b, void* pool, size_t page_by
                                  cudaStream_t stream) {
     if (b.n_pages <= kFusedPages) {
         const long vecs = (long)(data_bytes / 16);
-        pages_compact_kernel<<<fused_grid(b.n_pages / 2, vecs), kMoveThreads, 0, stream>>>(b, static_cast<char*>(pool),
-                                                                                         page_bytes, vecs);
-        return cudaGetLastError();
+        return launch_after(pages_compact_kernel, fused_grid(b.n_pages / 2, vecs), kMoveThreads, 0, stream, b,
+                            static_cast<char*>(pool), page_bytes, vecs);
     }
-    pages_compact_plan<<<1, kPlanThreads, 0, stream>>>(b);
+    const cudaError_t e = launch_after(pages_compact_plan, 1, kPlanThreads, 0, stream, b);
+    if (e != cudaSuccess) return e;
     return launch_moves(b, pool, page_bytes, data_bytes, stream);
 }
 
@@ -487,24 +492,21 @@ cudaError_t launch_pages_copy(const PagesBlock& b, void* pool, size_t page_bytes
     cudaError_t e;
     if (n <= kFusedList) {
         if ((e = set_smem_limit_once(pages_copy_kernel, kHeld, done_list)) != cudaSuccess) return e;
-        pages_copy_kernel<<<grid, kMoveThreads, held, stream>>>(b, source, dest, n, static_cast<char*>(pool), page_bytes,
-                                                                vecs, (int)width);
-        return cudaGetLastError();
+        return launch_after(pages_copy_kernel, grid, kMoveThreads, held, stream, b, source, dest, n,
+                            static_cast<char*>(pool), page_bytes, vecs, (int)width);
     }
-    pages_copy_plan<<<1, kPlanThreads, 0, stream>>>(b, source, dest, n);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(pages_copy_plan, 1, kPlanThreads, 0, stream, b, source, dest, n);
+    if (e != cudaSuccess) return e;
     if ((e = set_smem_limit_once(pages_strip_kernel, kHeld, done)) != cudaSuccess) return e;
-    pages_strip_kernel<<<grid, kMoveThreads, held, stream>>>(b, static_cast<char*>(pool), page_bytes, vecs, (int)width);
-    return cudaGetLastError();
+    return launch_after(pages_strip_kernel, grid, kMoveThreads, held, stream, b, static_cast<char*>(pool),
+                        page_bytes, vecs, (int)width);
 }
 
 cudaError_t launch_pages_rows(const PagesBlock& b, void* pool, size_t page_bytes, void* rows, size_t row_bytes,
                               const int* slots, int n, bool write, cudaStream_t stream) {
     const int pieces = (int)((row_bytes + 4095) / 4096);
-    pages_rows_kernel<<<(unsigned)((long)n * pieces), 256, 0, stream>>>(b, static_cast<char*>(pool), page_bytes,
-                                                                       static_cast<char*>(rows), row_bytes, slots, n,
-                                                                       pieces, write);
-    return cudaGetLastError();
+    return launch_after(pages_rows_kernel, (unsigned)((long)n * pieces), 256, 0, stream, b, static_cast<char*>(pool),
+                        page_bytes, static_cast<char*>(rows), row_bytes, slots, n, pieces, write);
 }
 
 }  // namespace efla

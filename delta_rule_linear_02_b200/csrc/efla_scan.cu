@@ -67,6 +67,7 @@ struct Geo {
     int per_head;      // strips of a head that is wider
     int strips, steps;
     int box;           // channels of one staged box: a head, or a strip's part of it
+    int planned;       // blocks that the plan counts on in a forward
 };
 
 // What a lane holds: channels c .. c + 3 of stream z, run `run` of each tile.
@@ -416,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
     const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
     const int* cu = P.by_value ? offsets.cu : P.cu;
     if (threadIdx.x == 0) {
-        if (P.clear_err && blockIdx.x == 0) *P.err = kDevOk;
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1);
         mbar_init(ready, kWarps);
         mbar_init(entered, kChainThreads / 32);
@@ -425,6 +425,8 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         fence_mbar_init();
     }
     __syncthreads();
+    after_previous(P.next);
+    if (P.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *P.err = kDevOk;
     const Stager stager(G, P.Z, P.T, strip);
     auto prefetch = [&](int n) {      // by the last warp
         const int chunk = n * blocks + rank;
@@ -586,7 +588,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     const int strip = blockIdx.x / blocks, turns = (G.steps + blocks - 1) / blocks;
     const int* cu = P.by_value ? offsets.cu : P.cu;
     if (threadIdx.x == 0) {
-        if (P.clear_err && blockIdx.x == 0) *P.err = kDevOk;
         for (int i = 0; i < M::kStages; ++i) mbar_init(full + i, 1), mbar_init(spent + i, kWarps);
         mbar_init(ready, kWarps);
         mbar_init(entered, kChainThreads / 32);
@@ -595,6 +596,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
         fence_mbar_init();
     }
     __syncthreads();
+    after_previous(P.next);
+    if (P.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *P.err = kDevOk;
     const Stager stager(G, P.Z, P.T, strip);
     auto prefetch = [&](int n) {
         const int chunk = G.steps - 1 - (n * blocks + rank);
@@ -770,8 +773,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
     if (blocks > 1) cluster_sync();
 }
 
-__global__ void __launch_bounds__(256) scan_parts_kernel(const float* __restrict__ parts, float* __restrict__ dg,
+__global__ void __launch_bounds__(256) scan_parts_kernel(const float* parts, float* dg,
                                                          long n, int count) {
+    after_previous();
     for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
         float sum = parts[i];
         for (int p = 1; p < count; ++p) sum += parts[p * n + i];
@@ -782,9 +786,10 @@ __global__ void __launch_bounds__(256) scan_parts_kernel(const float* __restrict
 // One token: a thread per four channels of a row, all loads at once.  Launch and latency are what it takes: 256 rows of
 // 16 heads of 128 in pages, 8.4 MB, 3.7 us; 4 rows of 4 heads of 64 2.9 us.
 template <typename Tin>
-__global__ void __launch_bounds__(256) scan_step_kernel(const Tin* __restrict__ x, const float* __restrict__ g,
-                                                        float* S, Tin* __restrict__ o, int N, int H, int d, int gw,
+__global__ void __launch_bounds__(256) scan_step_kernel(const Tin* x, const float* g,
+                                                        float* S, Tin* o, int N, int H, int d, int gw,
                                                         int rule, PagedRows P, bool paged, int pieces) {
+    after_previous();
     const int n = blockIdx.x / pieces;
     const int j = ((blockIdx.x % pieces) * 256 + threadIdx.x) * 4;      // channel of the row's H * d
     const long row = (long)n * H * d;
@@ -816,6 +821,9 @@ double scan_cost(long strips, long steps, int groups, int blocks, long held, lon
     return (double)(rounds * turns) * (0.75 + 0.53 * (double)share + exchange);
 }
 
+constexpr long kPlaces = 444;      // of forward blocks, three on each of 148 SMs
+bool lies_evenly(long grid, long places) { return 3 * grid <= places || 4 * grid >= 3 * places; }
+
 // The strips' width: the one with the least time at its best number of blocks, on 148 SMs with
 // three blocks each.  (64 heads of 128, T 2048: 37.5 us at width 128 with four blocks, 34 at 32 with
 // one; 16 heads, T 32768: 263 us at 128 with eight, 133 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
@@ -840,8 +848,8 @@ Geo scan_geo(long Z, int T, int d) {
         G.box = d < G.width ? d : G.width;
         double cost = 0;
         for (int b = 1; b <= kCluster && (b == 1 || b <= G.steps); ++b) {
-            const double c = scan_cost(G.strips, G.steps, groups, b, 444 / b, 148);
-            if (b == 1 || c < cost) cost = c;
+            const double c = scan_cost(G.strips, G.steps, groups, b, kPlaces / b, 148);
+            if (b == 1 || c < cost) cost = c, G.planned = G.strips * b;
         }
         if (groups == 1 || cost < least) best = G, least = cost;
     }
@@ -872,7 +880,7 @@ struct Room {
 };
 
 template <typename Kernel>
-void config(Kernel, int blocks, int smem, long strips, cudaStream_t stream, cudaLaunchConfig_t* cfg,
+void config(Kernel, int blocks, int smem, long strips, bool early, cudaStream_t stream, cudaLaunchConfig_t* cfg,
             cudaLaunchAttribute* attr) {
     *cfg = cudaLaunchConfig_t{};
     cfg->gridDim = dim3((unsigned)(strips * blocks));
@@ -882,8 +890,10 @@ void config(Kernel, int blocks, int smem, long strips, cudaStream_t stream, cuda
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg->attrs = attr;
-    cfg->numAttrs = blocks > 1 ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = blocks > 1 ? attr : attr + 1;
+    cfg->numAttrs = (blocks > 1) + early;
 }
 
 template <typename Kernel>
@@ -900,8 +910,8 @@ cudaError_t find_room(Kernel kernel, int (*smem)(int), Room* room) {
             n *= sms;
         } else {
             cudaLaunchConfig_t cfg;
-            cudaLaunchAttribute attr[1];
-            config(kernel, b, smem(b), 64, nullptr, &cfg, attr);
+            cudaLaunchAttribute attr[2];
+            config(kernel, b, smem(b), 64, false, nullptr, &cfg, attr);
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
                 cudaGetLastError();       // a size that this device does not run
                 n = 0;
@@ -955,10 +965,20 @@ cudaError_t launch_clusters(Kernel kernel, int (*smem)(int), Room* rooms, const 
     Offsets offsets;
     if (a.by_value) memcpy(offsets.cu, a.cu, ((size_t)a.nseq + 1) * sizeof(int));
     const int blocks = pick_blocks(room, G);
+    // A scan that is set up while this one runs takes the places that this one leaves free, and its blocks may lie unevenly:
+    // a layer's prefill of 256 blocks for 444 places takes 39.4 us instead of 32.6 so, and behind a backward that lets it in
+    // a training step 101 instead of 92.5.  With 384 blocks there is a gain (a training step with shared decays 62.6 -> 57.0),
+    // with one per SM at most too (short prompt 5.0 -> 4.5).  So a scan lets the next one in if a scan of its kind
+    // and a forward of its shape, which is what follows a backward, are of those sizes.
+    ScanArgs args = a;
+    args.next = lies_evenly((long)G.strips * blocks, room.clusters[1].load(std::memory_order_relaxed)) &&
+                lies_evenly(G.planned, kPlaces);
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
-    config(kernel, blocks, smem(blocks), G.strips, stream, &cfg, attr);
-    return cudaLaunchKernelEx(&cfg, kernel, a, maps, G, blocks, offsets);
+    cudaLaunchAttribute attr[2];
+    config(kernel, blocks, smem(blocks), G.strips, true, stream, &cfg, attr);
+    e = cudaLaunchKernelEx(&cfg, kernel, args, maps, G, blocks, offsets);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 template <typename Tin, bool kShared>
@@ -976,9 +996,8 @@ cudaError_t launch_bwd(const ScanArgs& a, cudaStream_t stream) {
         launch_clusters<Tin, kShared>(scan_bwd_kernel<Tin, kShared>, BwdSmem<Tin, kShared>::bytes, rooms, a, G, stream);
     if (e != cudaSuccess || !kShared || G.per_head == 1) return e;
     const long n = a.Z * a.T, blocks = (n + 255) / 256;
-    scan_parts_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(static_cast<const float*>(a.scratch),
-                                                                                    a.dg, n, G.per_head);
-    return cudaGetLastError();
+    return launch_after(scan_parts_kernel, (unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream,
+                        static_cast<const float*>(a.scratch), a.dg, n, G.per_head);
 }
 
 }  // namespace
@@ -999,12 +1018,10 @@ cudaError_t launch_scan_step(const void* x, const float* g, float* S, void* o, i
     const unsigned grid = (unsigned)((long)pieces * N);
     const PagedRows p = paged ? *paged : PagedRows();
     if (bf16)
-        scan_step_kernel<<<grid, 256, 0, stream>>>((const __nv_bfloat16*)x, g, S, (__nv_bfloat16*)o, N, H, d, gw, rule,
-                                                   p, paged != nullptr, pieces);
-    else
-        scan_step_kernel<<<grid, 256, 0, stream>>>((const float*)x, g, S, (float*)o, N, H, d, gw, rule, p,
-                                                   paged != nullptr, pieces);
-    return cudaGetLastError();
+        return launch_after(scan_step_kernel<__nv_bfloat16>, grid, 256, 0, stream, (const __nv_bfloat16*)x, g, S,
+                            (__nv_bfloat16*)o, N, H, d, gw, rule, p, paged != nullptr, pieces);
+    return launch_after(scan_step_kernel<float>, grid, 256, 0, stream, (const float*)x, g, S, (float*)o, N, H, d, gw,
+                            rule, p, paged != nullptr, pieces);
 }
 
 }  // namespace efla

@@ -99,6 +99,33 @@ __device__ __forceinline__ void scan_gates2(int rule, float2 g, float2* a, float
     if (rule == kRuleEuler) *w = both(1.0f), *dw = both(0.0f);
 }
 
+// The kernels of this family may be set up while the one before them in their stream still runs: launched by
+// launch_after, a kernel touches no global memory before after_previous(), which returns when the previous kernel has
+// ended and its writes are seen.  (No pointer of these kernels is __restrict__: loads marked as never changing might be
+// moved before it.)  With `next` it lets the next one be set up in turn while it runs: up to a us less for each call of a
+// run of them (a server's tick 27.8 -> 26.4 us, nine rows' delta step 6.7 -> 6.3, the short prompt 5.0 -> 4.5 on the device).
+__device__ __forceinline__ void after_previous(bool next = true) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (next) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                         Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+    if (e != cudaSuccess) cudaGetLastError();      // it is answered, not left for a later call
+    return e;
+}
+
 // Streams [Z][T][d] (dense: Z = B*H, one sequence each; packed: Z = H, sequences cu[n] ..
 // cu[n+1] of every stream); states [(n * Z + z) * d], n = 0 for dense batches.
 // Offsets of up to kScanInline sequences travel as a kernel argument: no copy before the launch (packed
@@ -124,6 +151,7 @@ struct ScanArgs {
     float* dS0 = nullptr;
     void* scratch = nullptr;
     uint32_t* err = nullptr;
+    bool next = false;              // the next kernel may be set up while this one runs (the launcher's choice)
     bool clear_err = true;          // the first kernel of a call forgets the last call's errors
 };
 size_t scan_states_bytes(long Z, int T, int d);

@@ -126,3 +126,71 @@ def test_refusals_on_the_gpu(efla, data):
     with pytest.raises(efla.EflaError):
         efla.efla_scan_fwd(D["X"], D["G"], rule=7)
     assert efla.efla_pages_status(pages) == efla.EFLA_OK
+
+
+def test_runs_of_calls_without_waiting(efla, data):
+    """Calls that each need the one before, of the library and of PyTorch in turn, queued at once: the bits of the same
+    calls with a wait after each."""
+    D, pages = data, data["pages"]
+    ones = torch.tensor([1, 2, 3], dtype=torch.int32, device="cuda")
+    zero = torch.full_like(ones, -1)
+    x = D["x"][:3].contiguous()
+    state = (D["pool"], D["mats"], pages.block)
+    before = [t.clone() for t in state]
+
+    def run(wait):
+        for t, b in zip(state, before):
+            t.copy_(b)
+        done, X = [], D["X"].clone()
+        mark = (lambda *t: (done.extend(t), torch.cuda.synchronize())) if wait else (lambda *t: done.extend(t))
+        for i in range(40):
+            o = efla.efla_scan_step_paged(x, D["g"][:3].contiguous(), pages, D["pool"], ones)
+            mark(o)
+            oo, S_T, saved = efla.efla_scan_fwd_save(X, D["G"], S0=D["S0"])
+            mark(oo, S_T)
+            grads = efla.efla_scan_backward(X, D["G"], oo, S0=D["S0"], saved=saved)
+            mark(*grads)
+            X = torch.tanh(grads[0]).to(X.dtype)
+            r = efla.efla_recurrent_step_paged(D["q"], D["k"], D["v"], D["beta"], pages, D["mats"], D["slots"])
+            mark(r)
+            efla.efla_pages_free(pages, ones)
+            mark()
+            efla.efla_pages_compact(pages, D["mats"])
+            mark()
+            efla.efla_pages_fork(pages, D["mats"], zero if i % 3 == 0 else zero + 5, ones)
+            mark()
+            efla.efla_pages_copy(pages, D["mats"], ones.flip(0), ones)
+            mark(efla.efla_pages_read(pages, D["mats"], ones))
+            D["mats"].mul_(0.9)
+        torch.cuda.synchronize()
+        return [t.clone() for t in (*done, *state)]
+
+    want, got = run(True), run(False)
+    assert len(want) == len(got) and all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    for t, b in zip(state, before):
+        t.copy_(b)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        o = efla.efla_scan_step_paged(x, D["g"][:3].contiguous(), pages, D["pool"], ones)
+        efla.efla_pages_free(pages, ones)
+        efla.efla_pages_compact(pages, D["mats"])
+        efla.efla_pages_fork(pages, D["mats"], zero + 5, ones)
+        r = efla.efla_recurrent_step_paged(D["q"], D["k"], D["v"], D["beta"], pages, D["mats"], D["slots"])
+    for t, b in zip(state, before):
+        t.copy_(b)
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    captured = [t.clone() for t in (o, r, *state)]
+    for t, b in zip(state, before):
+        t.copy_(b)
+    for _ in range(20):
+        o = efla.efla_scan_step_paged(x, D["g"][:3].contiguous(), pages, D["pool"], ones)
+        efla.efla_pages_free(pages, ones)
+        efla.efla_pages_compact(pages, D["mats"])
+        efla.efla_pages_fork(pages, D["mats"], zero + 5, ones)
+        r = efla.efla_recurrent_step_paged(D["q"], D["k"], D["v"], D["beta"], pages, D["mats"], D["slots"])
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, (o, r, *state)))
+    assert efla.efla_pages_status(pages) == efla.EFLA_OK
