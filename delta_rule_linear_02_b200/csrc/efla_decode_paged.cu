@@ -5,7 +5,7 @@
 // Bound by memory: the state is read once and written once, 8 bytes for four flops.  Column j of the new
 // state needs column j of the old one alone: in the first kernel a block owns 32 columns of one head and passes
 // them through registers once, every load of it in flight at the start.  For few rows that is the
-// shortest way (9 rows of 16 heads of 128: 6.4 us for 19 MB); for many the second kernel is
+// shortest way (9 rows of 16 heads of 128: 6.3 us for 19 MB); for many the second kernel is
 // better, as blocks of one short life each leave memory idle between them.
 #include "efla_kernels.h"
 #include "efla_pages.cuh"
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const Tin* q, co
 // The same step for many heads.  A head's state is contiguous in its page, so a producer warp moves
 // 64 KiB jobs (one head of 128, four of 64) by bulk copies through a ring of three buffers, in and
 // out, and looks the rows up ahead; eight warps keep a job's state in registers from the first
-// product to the update and write it back in place.  256 rows of 16 heads of 128: 99 us, 5.5 TB/s read
-// and written (84% of the measured copy rate; the same state updated in place without pages: 95.6).
+// product to the update and write it back in place.  256 rows of 16 heads of 128: 98 us, 5.6 TB/s read
+// and written (85% of the measured copy rate; the same state updated in place without pages: 95.6).
 constexpr int kJobFloats = 16384, kRing = 3, kWorkers = 256, kStreamThreads = kWorkers + 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 

@@ -6,8 +6,9 @@
 //
 // For caches of up to 4096 pages and lists of up to 256 entries one launch does both: every block
 // makes the whole plan for itself in shared memory, moves its share, and the last one to finish writes
-// the new table and owners, which the others have by then read (48 pairs of 8 KiB copied: 8 us a call, 4.7 on
-// the device, with two launches 17; free, compact and fork of 24 of 256 pages of 1 MiB: 33 and 44).
+// the new table and owners, which the others have by then read (48 pairs of 8 KiB copied: 3.9 us; with two
+// launches the call took twice as long; free, compact and fork of 24 of 256 pages of 1 MiB: 26.6 us, with two launches each 11
+// more).
 // Larger ones take a launch of one block for the plan.
 #include "efla_kernels.h"
 #include "efla_pages.cuh"

@@ -13,8 +13,10 @@
 //   3. the compute warps continue their runs from there and write the outputs.
 // Bound by memory where there are strips enough (444 heads of 128, T 2048, bf16: 150 us, 6.2 TB/s, 95%
 // of the measured copy rate), by a turn's latency, about 2 us from its loads to the next state,
-// where there are few (64 heads: 33 us, 4.1 TB/s; 16 heads, T 32768: 132 us, 4.1 TB/s): strips as
-// narrow as 32 channels and clusters along time are there to have more turns in flight.
+// where there are few (64 heads: 32 us, 4.2 TB/s; 16 heads, T 32768: 130 us, 4.1 TB/s): strips as
+// narrow as 32 channels and clusters along time are there to have more turns in flight.  A turn of 64 heads' 3370
+// cycles: products 1400, fold 200, exchange 410, entering 240, outputs 600, waits 500; with six blocks in a cluster the
+// exchange, which waits for the slowest of them, takes 2300 of 5200.
 // Inputs are staged some turns ahead and read from memory once; tokens behind the end and
 // channels beside a head are staged as zeros, which change nothing (e^0 = 1, x = 0).  Everything
 // is folded in token order, so the results are the same bits on every run.
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
 // token), G_t = dO_t + c: affine again, c_out = A c_in + R over a run, and the tiles are taken
 // from the last to the first.  A tile's own states are put together again from the state that
 // the forward kept for it, so no other state is ever stored.  296 heads of 128, T 2048, bf16: 209 us,
-// 5.9 TB/s (90% of the measured copy rate); 64 heads: 60 us, 4.5 TB/s.  Three kinds of gate of four
+// 5.9 TB/s (90% of the measured copy rate); 64 heads: 61 us, 4.4 TB/s.  Three kinds of gate of four
 // tokens stay in registers from the products to the gradients: 96 of them a thread, two blocks on an SM.
 template <typename Tin, bool kShared>
 struct BwdSmem {
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(256) scan_parts_kernel(const float* parts, flo
 }
 
 // One token: a thread per four channels of a row, all loads at once.  Launch and latency are what it takes: 256 rows of
-// 16 heads of 128 in pages, 8.4 MB, 3.7 us; 4 rows of 4 heads of 64 2.9 us.
+// 16 heads of 128 in pages, 8.4 MB, 4.2 us one behind the other; 4 rows of 4 heads of 64 1.8 us.
 template <typename Tin>
 __global__ void __launch_bounds__(256) scan_step_kernel(const Tin* x, const float* g,
                                                         float* S, Tin* o, int N, int H, int d, int gw,

@@ -194,3 +194,27 @@ def test_runs_of_calls_without_waiting(efla, data):
         torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(captured, (o, r, *state)))
     assert efla.efla_pages_status(pages) == efla.EFLA_OK
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_states_in_place_through_queued_calls(efla, cuda, packed):
+    """A prompt in pieces, each from the state that the one before left in the same memory, queued at once."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    B, H, T, d = 3, 4, 1500, 128
+    cu = [0, 700, 700, T] if packed else None
+    lead = (H, T) if packed else (B, H, T)
+    x = torch.randn(*lead, d, generator=gen, device="cuda")
+    g = -0.01 * torch.rand(*lead, d, generator=gen, device="cuda")
+    S0 = torch.randn(B, H, d, generator=gen, device="cuda")
+
+    def run(wait):
+        S, out = S0.clone(), []
+        for _ in range(60):
+            out.append(efla.efla_scan_fwd(x, g, S0=S, S_T=S, cu_seqlens=cu)[0][..., -1, :].clone() if wait else
+                       efla.efla_scan_fwd(x, g, S0=S, S_T=S, cu_seqlens=cu)[0])
+            if wait:
+                torch.cuda.synchronize()
+        return [o if wait else o[..., -1, :].clone() for o in out] + [S]
+
+    want, got = run(True), run(False)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
