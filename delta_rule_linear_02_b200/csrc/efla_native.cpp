@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 
 #include <vector>
 
@@ -83,8 +84,9 @@ struct Place {
         need(c10::cuda::current_device() == dev);
         stream = c10::cuda::getCurrentCUDAStream(dev).stream();
     }
-    at::TensorOptions options(at::ScalarType type) const {
-        return at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, dev));
+    // (past the dispatcher, which takes longer than the allocation)
+    at::Tensor empty(at::ScalarType type, Sizes shape) const {
+        return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, dev), std::nullopt));
     }
 };
 
@@ -102,7 +104,8 @@ struct Output {
         object = given;
     }
     void make(const Place& at, at::ScalarType type, Sizes shape, bool zeros = false) {
-        at::Tensor t = zeros ? at::zeros(shape, at.options(type)) : at::empty(shape, at.options(type));
+        at::Tensor t = at.empty(type, shape);
+        if (zeros) t.zero_();
         p = t.data_ptr();
         object = THPVariable_Wrap(std::move(t));
         need(object);
@@ -292,7 +295,7 @@ PyObject* scan_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(PyBool_Check(a[8]));
         if (a[8] == Py_True) dS0.make(at, at::kFloat, s.state);
         else dS0.none();
-        const at::Tensor ws = at::empty(Sizes(&bytes, 1), at.options(at::kByte));
+        const at::Tensor ws = at.empty(at::kByte, Sizes(&bytes, 1));
         void* pws = ws.data_ptr();
         PyObject* out = PyTuple_New(3);
         need(out);
