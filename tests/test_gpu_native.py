@@ -218,3 +218,46 @@ def test_states_in_place_through_queued_calls(efla, cuda, packed):
 
     want, got = run(True), run(False)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_two_streams_that_wait_for_each_other(efla, cuda):
+    """Calls on two streams that need each other's results through events, queued at once, and the same captured."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    x, g, S0 = r(2, 4, 900, 64), -0.1 * r(2, 4, 900).abs(), r(2, 4, 64)
+    xt, gt = r(2, 4, 64), -0.1 * r(2, 4, 64).abs()
+    other = torch.cuda.Stream()
+    S = S0.clone()
+
+    def turn():      # here: a prompt's piece; there: a token on its state; here again: the next piece
+        main = torch.cuda.current_stream()
+        efla.efla_scan_fwd(x, g, S0=S, S_T=S)
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            o = efla.efla_scan_step(xt, gt, S)
+            torch.mul(S, 0.5, out=S)
+            o2 = efla.efla_scan_step(xt, gt, S)
+        main.wait_stream(other)
+        out = efla.efla_scan_fwd(x, g, S0=S, S_T=S)[0]
+        return o, o2, out
+
+    def run(wait):
+        S.copy_(S0)
+        keep = []
+        for _ in range(30):
+            keep.append(turn())
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [t.clone() for ts in keep for t in ts] + [S.clone()]
+
+    want, got = run(True), run(False)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = turn()
+    S.copy_(S0)
+    for _ in range(30):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*outs, S), want[-4:]))
