@@ -214,6 +214,14 @@ __device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
     return words[run >> 3] >> (run & 7) * kRun & ((1u << kRun) - 1u);
 }
 
+// Whether a warp's runs of a tile have any mark.
+__device__ __forceinline__ bool warp_marked(const MarkRing* ring, int slot, int warp, const Geo& G) {
+    if (!ring->any[slot]) return false;
+    const int bits = G.groups * kRun, at = warp * bits;       // 4, 8 or 16 tokens
+    const Marks& m = ring->m[slot];
+    return (m.first[at >> 5] | m.last[at >> 5]) >> (at & 31) & ((1u << bits) - 1u);
+}
+
 // Sequences without tokens pass their states through.
 __device__ __forceinline__ void pass_empty(const ScanArgs& P, const int* cu, const float* in, float* out) {
     if (!cu || !out) return;
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
             wait_or_give_up(full + st, n / M::kStages & 1, &dead, P.err);
             const Tin* xs = x0 + st * (M::kStage / (int)sizeof(Tin));
             const float* gt = g0 + st * (M::kStage / 4);
-            // most tiles have no begin or end of a sequence in them; their code knows it, and the rule
+            // most runs have no begin or end of a sequence in them; their code knows it, and the rule
             auto tile = [&](auto plain_, auto rule_) {
                 constexpr bool plain = decltype(plain_)::value;
                 const int rule = decltype(rule_)::value < 0 ? P.rule : decltype(rule_)::value;
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                         st4(P.S_T + ((long)seqs[i] * P.Z + L.z) * P.d + L.c, h);
                 }
             };
-            if (ring->any[n % kMarks]) tile(std::false_type(), std::integral_constant<int, -1>());
+            if (warp_marked(ring, n % kMarks, warp, G)) tile(std::false_type(), std::integral_constant<int, -1>());
             else if (P.rule == kRuleExact) tile(std::true_type(), std::integral_constant<int, kRuleExact>());
             else tile(std::true_type(), std::integral_constant<int, kRuleEuler>());
         }
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
                     sum_tokens(sum, to, span, lane, L.z < P.Z ? P.T - tw : 0);
                 }
             };
-            if (ring->any[n % kMarks]) tile(std::false_type(), std::integral_constant<int, -1>());
+            if (warp_marked(ring, n % kMarks, warp, G)) tile(std::false_type(), std::integral_constant<int, -1>());
             else if (P.rule == kRuleExact) tile(std::true_type(), std::integral_constant<int, kRuleExact>());
             else tile(std::true_type(), std::integral_constant<int, kRuleEuler>());
             warp_arrive(spent + st);
