@@ -157,6 +157,7 @@ struct Marks {
 struct MarkRing {
     Marks m[kMarks];
     uint32_t any[kMarks];
+    int2 extent[32];       // of a lane's sequence, where there are up to 32 of them
 };
 // The part of a row of states that a strip reads, towards this SM.
 struct StateRow {
@@ -171,16 +172,17 @@ struct StateRow {
 };
 // One warp: the sequences from the one that holds t0 on, a lane each.  (A call, so that what few
 // tiles need costs the kernels no registers.)
-__device__ __noinline__ bool find_marks(const int* cu, int nseq, int T, int t0, int t1, StateRow begins, StateRow ends,
+__device__ __noinline__ bool find_marks(const int* cu, int nseq, int2 own, int t0, int t1, StateRow begins, StateRow ends,
                                         Marks* m) {
     const int lane = threadIdx.x & 31;
+    const bool few = nseq <= 32;
     uint32_t* words = m->first;                // and m->last behind it
     if (lane < 8) words[lane] = 0;
     __syncwarp();
     bool any = false;
-    for (int n0 = cu ? seq_of(cu, nseq, t0) : 0;; n0 += 32) {
+    for (int n0 = few ? 0 : seq_of(cu, nseq, t0);; n0 += 32) {
         const int n = n0 + lane;
-        const int from = n >= nseq ? t1 : cu ? cu[n] : 0, to = n >= nseq ? t1 : cu ? cu[n + 1] : T;
+        const int from = few ? own.x : n >= nseq ? t1 : cu[n], to = few ? own.y : n >= nseq ? t1 : cu[n + 1];
         if (from < to && from >= t0 && from < t1) {
             atomicOr(words + ((from - t0) >> 5), 1u << ((from - t0) & 31));
             m->seq[from - t0] = n;
@@ -193,19 +195,26 @@ __device__ __noinline__ bool find_marks(const int* cu, int nseq, int T, int t0, 
             ends.prefetch(n);
             any = true;
         }
-        if (__any_sync(0xffffffffu, from >= t1)) break;
+        if (few || __any_sync(0xffffffffu, from >= t1)) break;
     }
     return __any_sync(0xffffffffu, any);
 }
-__device__ __forceinline__ void make_marks(const ScanArgs& P, const int* cu, const Stager& S, int chunk,
-                                           const float* begins, const float* ends, MarkRing* ring, int slot) {
-    const int t0 = chunk * S.G.tokens, left = P.T - t0;
-    bool any = false;
-    if (cu || t0 == 0 || left <= S.G.tokens) {
+// Held by the staging warp for itself: looked up for every tile, the offsets cost it, and with it the next turn, two
+// loads one behind the other (packed requests 78.4 us instead of 75).
+__device__ __forceinline__ void hold_extents(const int* cu, int nseq, int T, MarkRing* ring) {
+    const int n = threadIdx.x & 31;
+    ring->extent[n] = n < nseq ? (cu ? make_int2(cu[n], cu[n + 1]) : make_int2(0, T)) : make_int2(0, 0);
+}
+__device__ __forceinline__ void make_marks(const ScanArgs& P, const int* cu, const Stager& S, int chunk, const float* begins,
+                                           const float* ends, MarkRing* ring, int slot) {
+    const int t0 = chunk * S.G.tokens, t1 = t0 + min(S.G.tokens, P.T - t0), nseq = cu ? P.nseq : 1;
+    const int2 own = ring->extent[threadIdx.x & 31];
+    bool any = nseq > 32 || __any_sync(0xffffffffu, own.x < own.y && ((own.x >= t0 && own.x < t1) ||
+                                                                          (own.y > t0 && own.y <= t1)));
+    if (any) {
         const long at = (long)S.z0 * P.d + S.c0, row = P.Z * P.d;
         const int floats = (int)min((long)(S.G.per_head > 1 ? min(S.G.width, P.d - S.c0) : S.heads * P.d), row - at);
-        any = find_marks(cu, cu ? P.nseq : 1, P.T, t0, t0 + min(S.G.tokens, left),
-                         StateRow{begins ? begins + at : nullptr, row, floats},
+        any = find_marks(cu, nseq, own, t0, t1, StateRow{begins ? begins + at : nullptr, row, floats},
                          StateRow{ends ? ends + at : nullptr, row, floats}, ring->m + slot);
     }
     if ((threadIdx.x & 31) == 0) ring->any[slot] = any;
@@ -454,8 +463,10 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         stager.stage(dx, static_cast<const Tin*>(P.x), &maps.x, t0, full + st);
         if (!kShared) stager.stage(dg, P.g, &maps.g, t0, full + st);
     };
-    if (warp == kThreads / 32 - 1)
+    if (warp == kThreads / 32 - 1) {
+        hold_extents(cu, cu ? P.nseq : 1, P.T, ring);
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
+    }
     pass_empty(P, cu, P.S0, P.S_T);
     if (blocks > 1) cluster_sync();       // every block's barriers are set up
     bool dead = false;
@@ -627,8 +638,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs P, const
         stager.stage(sx + kValues, static_cast<const Tin*>(P.dO), &maps.dO, t0, full + st);
         if (!kShared) stager.stage(sg, P.g, &maps.g, t0, full + st);
     };
-    if (warp == kThreads / 32 - 1)
+    if (warp == kThreads / 32 - 1) {
+        hold_extents(cu, cu ? P.nseq : 1, P.T, ring);
         for (int i = 0; i < M::kStages; ++i) prefetch(i);
+    }
     pass_empty(P, cu, P.dST, P.dS0);
     if (blocks > 1) cluster_sync();
     bool dead = false;
