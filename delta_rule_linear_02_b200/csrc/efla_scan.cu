@@ -266,6 +266,10 @@ __device__ __forceinline__ Fold fold_runs(const float* runA, const float* runB, 
     if (cut) f.A = both(kCut);
     return f;
 }
+__device__ __forceinline__ Fold fold_two(const Fold& f, const Fold& then) {
+    const bool cut = is_cut(f.A.x) || is_cut(then.A.x);
+    return Fold{cut ? both(kCut) : mul2(f.A, then.A), run_on(then.A, f.B, then.B)};
+}
 template <bool kReverse>
 __device__ __forceinline__ void enter_runs(const float* runA, float* runB, int width, float2 h) {
     float2 A[8], B[8];
@@ -346,6 +350,32 @@ __device__ __forceinline__ float2 chain_turn(const Fold& f, int blocks, const Ge
     }
     *carry = h;
     return mine;
+}
+
+// The same for a forward's strip of 32 channels in a cluster: of its four parts a warp has two and sends them as one, each
+// half of it to every other block (the long document 130.8 -> 123.8 us.  Within one block, and in the backward, whose
+// registers it takes, it costs more than it gives: layer prefill 32.2 -> 34.5).
+__device__ __forceinline__ float2 chain_turn_pairs(const Fold& f, int blocks, int rank, int n, float4* sent, uint64_t* got,
+                                                   float2* carry, bool* dead, uint32_t* err) {
+    const int lane = threadIdx.x & 31, place = rank * 2 + (threadIdx.x >> 5 & 1), buf = n & 1;
+    const bool second = lane >= 16;
+    const Fold other{make_float2(__shfl_xor_sync(0xffffffffu, f.A.x, 16), __shfl_xor_sync(0xffffffffu, f.A.y, 16)),
+                     make_float2(__shfl_xor_sync(0xffffffffu, f.B.x, 16), __shfl_xor_sync(0xffffffffu, f.B.y, 16))};
+    const Fold whole = second ? fold_two(other, f) : fold_two(f, other);
+    float4* all = sent + buf * blocks * kChainThreads + (lane & 15);
+    const uint32_t to = smem_u32(all + place * 16), bar = smem_u32(got + buf);
+    for (int q = second; q < blocks; q += 2) send(in_block(to, q), in_block(bar, q), whole.A, whole.B);
+    if (threadIdx.x == kComputeThreads) mbar_arrive_expect_tx(got + buf, blocks * 2 * 16 * 16);
+    wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
+    float2 h = *carry, mine = h;
+#pragma unroll 4
+    for (int q = 0; q < 2 * blocks; ++q) {
+        const float4 v = all[q * 16];
+        if (q == place) mine = h;
+        h = run_on(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
+    }
+    *carry = h;
+    return second ? run_on(other.A, mine, other.B) : mine;
 }
 
 // The gates of one token: of a channel each, or one for all.
@@ -484,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                 wait_or_give_up(ready, n & 1, &dead, P.err);
                 f = fold_runs<false>(runA, runB, G.width);
             }
-            const float2 h = chain_turn(f, blocks, G, rank * G.groups + part, pair, n, sent, got, &carry, &dead, P.err);
+            const float2 h = G.groups == 4 && blocks > 1
+                                 ? chain_turn_pairs(f, blocks, rank, n, sent, got, &carry, &dead, P.err)
+                                 : chain_turn(f, blocks, G, rank * G.groups + part, pair, n, sent, got, &carry, &dead, P.err);
             if (tile) {
                 enter_runs<false>(runA, runB, G.width, h);
                 warp_arrive(entered);
