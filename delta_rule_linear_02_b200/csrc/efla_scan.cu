@@ -13,10 +13,10 @@
 //   3. the compute warps continue their runs from there and write the outputs.
 // Bound by memory where there are strips enough (444 heads of 128, T 2048, bf16: 150 us, 6.2 TB/s, 95%
 // of the measured copy rate), by a turn's latency, about 2 us from its loads to the next state,
-// where there are few (64 heads: 32 us, 4.2 TB/s; 16 heads, T 32768: 130 us, 4.1 TB/s): strips as
+// where there are few (64 heads: 32 us, 4.2 TB/s; 16 heads, T 32768: 123 us, 4.4 TB/s): strips as
 // narrow as 32 channels and clusters along time are there to have more turns in flight.  A turn of 64 heads' 3370
-// cycles: products 1400, fold 200, exchange 410, entering 240, outputs 600, waits 500; with six blocks in a cluster the
-// exchange, which waits for the slowest of them, takes 2300 of 5200.
+// cycles: products 1400, fold 200, exchange 410, entering 240, outputs 600, waits 500; with six blocks in a cluster a turn
+// takes about 4900, half of them the exchange, which waits for the slowest block.
 // Inputs are staged some turns ahead and read from memory once; tokens behind the end and
 // channels beside a head are staged as zeros, which change nothing (e^0 = 1, x = 0).  Everything
 // is folded in token order, so the results are the same bits on every run.
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
 // token), G_t = dO_t + c: affine again, c_out = A c_in + R over a run, and the tiles are taken
 // from the last to the first.  A tile's own states are put together again from the state that
 // the forward kept for it, so no other state is ever stored.  296 heads of 128, T 2048, bf16: 209 us,
-// 5.9 TB/s (90% of the measured copy rate); 64 heads: 61 us, 4.4 TB/s.  Three kinds of gate of four
+// 5.9 TB/s (90% of the measured copy rate); 64 heads: 60 us, 4.5 TB/s.  Three kinds of gate of four
 // tokens stay in registers from the products to the gradients: 96 of them a thread, two blocks on an SM.
 template <typename Tin, bool kShared>
 struct BwdSmem {
@@ -881,7 +881,7 @@ bool lies_evenly(long grid, long places) { return 3 * grid <= places || 4 * grid
 
 // The strips' width: the one with the least time at its best number of blocks, on 148 SMs with
 // three blocks each.  (64 heads of 128, T 2048: 37.5 us at width 128 with four blocks, 34 at 32 with
-// one; 16 heads, T 32768: 263 us at 128 with eight, 133 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
+// one; 16 heads, T 32768: 263 us at 128 with eight, 123 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
 Geo scan_geo(long Z, int T, int d) {
     static thread_local struct {
         long Z;
