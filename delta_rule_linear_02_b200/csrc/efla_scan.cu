@@ -251,6 +251,7 @@ __device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast
 struct Fold {
     float2 A, B;
 };
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 template <bool kReverse>
 __device__ __forceinline__ Fold fold_runs(const float* runA, const float* runB, int width) {
     Fold f{both(1.f), both(0.f)};
@@ -355,24 +356,68 @@ __device__ __forceinline__ float2 chain_turn(const Fold& f, int blocks, const Ge
 // The same for a forward's strip of 32 channels in a cluster: of its four parts a warp has two and sends them as one, each
 // half of it to every other block (the long document 130.8 -> 123.8 us.  Within one block, and in the backward, whose
 // registers it takes, it costs more than it gives: layer prefill 32.2 -> 34.5).
-__device__ __forceinline__ float2 chain_turn_pairs(const Fold& f, int blocks, int rank, int n, float4* sent, uint64_t* got,
-                                                   float2* carry, bool* dead, uint32_t* err) {
+// The decays of two parts, 64 tokens, may multiply to more than fp32 holds where those of each do not (growth), and so may
+// what they leave of their inputs.  The state behind such a pair is then not finite, whatever entered it.  All warps of the
+// cluster read all pairs of the strip, so all see it, and the parts follow (as they do where inputs are not finite).  To look
+// for it costs a turn 0.05 us (the long document 122.7 -> 125.0 in a graph of calls); parts sent apart always take 131.7.
+struct Parts {
+    float2 mine, h;            // the state entering the warp's own pair, and the last one
+    bool dead;
+};
+// Folds the turn's pairs onto h, those that fp32 does not hold part by part.  The parts go to the second half of `sent`,
+// counted by a barrier of their own: every block has read one turn's parts before it sends the next turn's pairs, and no
+// block sends parts again before it has got these.  A channel's state comes from its own pairs and parts alone.  (A call,
+// so that what few streams need costs the kernels few registers.)
+__device__ __noinline__ Parts fold_parts(Fold f, float2 h, int blocks, int place, const float4* pairs, float4* sent,
+                                         uint64_t* got, bool dead, uint32_t* err) {
+    const int lane = threadIdx.x & 31, second = lane >> 4;
+    int* turns = reinterpret_cast<int*>(got + 1) + (place & 1);      // this warp's earlier ones
+    const int phase = *turns & 1;
+    float4* parts = sent + blocks * kChainThreads + (lane & 15);
+    const uint32_t to = smem_u32(parts + (2 * place + second) * 16), bar = smem_u32(got);
+    for (int q = 0; q < blocks; ++q) send(in_block(to, q), in_block(bar, q), f.A, f.B);
+    if (threadIdx.x == kComputeThreads) mbar_arrive_expect_tx(got, blocks * kChainThreads * 16);
+    __syncwarp();
+    if (lane == 0) ++*turns;
+    wait_or_give_up(got, phase, &dead, err);
+    float2 now = h, mine = now;
+#pragma unroll 1
+    for (int q = 0; q < 2 * blocks; ++q) {
+        const float4 v = pairs[q * 16], p = parts[q * 32], r = parts[q * 32 + 16];
+        if (q == place) mine = now;
+        const float2 one = run_on(make_float2(v.x, v.y), now, make_float2(v.z, v.w));
+        now = run_on(make_float2(p.x, p.y), now, make_float2(p.z, p.w));
+        now = run_on(make_float2(r.x, r.y), now, make_float2(r.z, r.w));
+        if (is_finite(v.x) && is_finite(v.z)) now.x = one.x;
+        if (is_finite(v.y) && is_finite(v.w)) now.y = one.y;
+    }
+    return Parts{mine, now, dead};
+}
+__device__ __forceinline__ float2 chain_turn_pairs(const Fold& f, int blocks, int rank, int n, float4* sent,
+                                                   uint64_t* got, float2* carry, bool* dead, uint32_t* err) {
     const int lane = threadIdx.x & 31, place = rank * 2 + (threadIdx.x >> 5 & 1), buf = n & 1;
     const bool second = lane >= 16;
     const Fold other{make_float2(__shfl_xor_sync(0xffffffffu, f.A.x, 16), __shfl_xor_sync(0xffffffffu, f.A.y, 16)),
                      make_float2(__shfl_xor_sync(0xffffffffu, f.B.x, 16), __shfl_xor_sync(0xffffffffu, f.B.y, 16))};
     const Fold whole = second ? fold_two(other, f) : fold_two(f, other);
-    float4* all = sent + buf * blocks * kChainThreads + (lane & 15);
+    float4* all = sent + buf * blocks * (kChainThreads / 2) + (lane & 15);
     const uint32_t to = smem_u32(all + place * 16), bar = smem_u32(got + buf);
     for (int q = second; q < blocks; q += 2) send(in_block(to, q), in_block(bar, q), whole.A, whole.B);
     if (threadIdx.x == kComputeThreads) mbar_arrive_expect_tx(got + buf, blocks * 2 * 16 * 16);
     wait_or_give_up(got + buf, n >> 1 & 1, dead, err);
-    float2 h = *carry, mine = h;
+    float2 h = *carry, mine = h, zero = both(0.f);      // zero: until a state is not finite, NaN from there on
 #pragma unroll 4
     for (int q = 0; q < 2 * blocks; ++q) {
         const float4 v = all[q * 16];
         if (q == place) mine = h;
         h = run_on(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
+        zero = fma2(h, both(0.f), zero);
+    }
+    if (__any_sync(0xffffffffu, zero.x + zero.y != 0.f)) {
+        const Parts parts = fold_parts(f, *carry, blocks, place, all, sent, got + 2, *dead, err);
+        mine = parts.mine;
+        h = parts.h;
+        *dead = parts.dead;
     }
     *carry = h;
     return second ? run_on(other.A, mine, other.B) : mine;
@@ -459,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
     uint64_t* full = reinterpret_cast<uint64_t*>(sent + 2 * blocks * kChainThreads);
     uint64_t* ready = full + M::kStages;      // the tile's (A, B) of all runs are there
     uint64_t* entered = ready + 1;            // the states entering them are
-    uint64_t* got = entered + 1;              // [2] all blocks' (A, B) are
+    uint64_t* got = entered + 1;              // [2] all blocks' (A, B) are; the parts of pairs
     MarkRing* ring = reinterpret_cast<MarkRing*>(full + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blocks > 1 ? (int)cluster_rank() : 0;
@@ -471,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         mbar_init(entered, kChainThreads / 32);
         mbar_init(got, 1);
         mbar_init(got + 1, 1);
+        mbar_init(got + 2, 1);
+        got[3] = 0;               // how often parts have followed, by warp
         fence_mbar_init();
     }
     __syncthreads();
@@ -505,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
         const int k = threadIdx.x - kComputeThreads, pair = k % (G.width / 2), part = k / (G.width / 2);
         float* runA = runs + part * 8 * G.width + pair * 2;
         float* runB = runA + M::kRuns;
+        const bool pairs = G.groups == 4 && blocks > 1;
         float2 carry = both(0.f);
         for (int n = 0; n < turns; ++n) {
             const int chunk = n * blocks + rank;
@@ -514,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
                 wait_or_give_up(ready, n & 1, &dead, P.err);
                 f = fold_runs<false>(runA, runB, G.width);
             }
-            const float2 h = G.groups == 4 && blocks > 1
-                                 ? chain_turn_pairs(f, blocks, rank, n, sent, got, &carry, &dead, P.err)
-                                 : chain_turn(f, blocks, G, rank * G.groups + part, pair, n, sent, got, &carry, &dead, P.err);
+            const float2 h = pairs ? chain_turn_pairs(f, blocks, rank, n, sent, got, &carry, &dead, P.err)
+                                   : chain_turn(f, blocks, G, rank * G.groups + part, pair, n, sent, got, &carry, &dead,
+                                                P.err);
             if (tile) {
                 enter_runs<false>(runA, runB, G.width, h);
                 warp_arrive(entered);
