@@ -7,6 +7,7 @@ it has not been built (python delta_rule_linear_02_b200/build.py).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -534,21 +535,32 @@ def _made(out, where: str) -> bool:
     return True
 
 
-def _made_here(stream, *tensors) -> None:
-    """Tensors that a call allocated itself and uses on `stream`: their memory is not given away before it has run."""
+def _made_on(stream, device: torch.device):
+    """The context in which a call on `stream` makes its tensors: in that stream's memory, which no work queued on
+    another one still uses (None: the current stream's)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _handed_over(stream, device: torch.device, *tensors) -> None:
+    """Results in another stream's memory: it is not given away before the current stream is done with them."""
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        current = torch.cuda.current_stream(device)
         for t in tensors:
             if t is not None:
-                t.record_stream(s)
+                t.record_stream(current)
 
 
 def _zeros(like: torch.Tensor, shape, stream) -> torch.Tensor:
     """Zeros made on `stream` (None: the current one), so that the call that fills them comes after."""
-    if stream is None:
-        return like.new_zeros(shape)
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
-        return like.new_zeros(shape)
+    with _made_on(stream, like.device):
+        out = like.new_zeros(shape)
+    _handed_over(stream, like.device, out)
+    return out
 
 
 def _tensor(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optional[int]:
@@ -603,28 +615,24 @@ def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule)
         raise ValueError(f"x must be on a CUDA device, got {dev}")
     px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", f32, dev, g.shape)
     pS0 = _tensor(S0, "S0", f32, dev, (B, H, d))
-    if o is None:
-        o = torch.empty_like(x)
-        po = o.data_ptr()
-        _made_here(stream, o)
-    else:
-        po = _tensor(o, "o", x.dtype, dev, x.shape)
-    if S_T is None and want_state:
-        S_T = x.new_empty((B, H, d), dtype=f32)
-        pS_T = S_T.data_ptr()
-        _made_here(stream, S_T)
-    else:
-        pS_T = _tensor(S_T, "S_T", f32, dev, (B, H, d))
-    if workspace is None:
-        n = lib.efla_scan_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None))
-        if n == 0:
-            raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_workspace_bytes")
-        workspace = x.new_empty(n, dtype=torch.uint8)
-        pw = workspace.data_ptr()
-        _made_here(stream, workspace)
-    else:
-        n = workspace.numel()
-        pw = _tensor(workspace, "workspace", torch.uint8, dev, (n,))
+    made = []
+    with _made_on(stream, dev):
+        if o is None:
+            o = torch.empty_like(x)
+            made.append(o)
+        if S_T is None and want_state:
+            S_T = x.new_empty((B, H, d), dtype=f32)
+            made.append(S_T)
+        if workspace is None:
+            n = lib.efla_scan_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None))
+            if n == 0:
+                raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_workspace_bytes")
+            workspace = x.new_empty(n, dtype=torch.uint8)
+            made.append(workspace)
+    _handed_over(stream, dev, *made)
+    po, pS_T = _tensor(o, "o", x.dtype, dev, x.shape), _tensor(S_T, "S_T", f32, dev, (B, H, d))
+    n = workspace.numel()
+    pw = _tensor(workspace, "workspace", torch.uint8, dev, (n,))
     _call(lib.efla_scan_fwd, "efla_scan_fwd", dev, stream, px, pg, None if cu is None else cu.data_ptr(), pS0, po, pS_T,
           B, H, T, d, gw, dt, int(rule), pw, n)
     return o, S_T, workspace
@@ -637,6 +645,8 @@ def efla_scan_fwd(x, g, S0=None, cu_seqlens=None, o=None, S_T=None, workspace=No
     None.  Packed: cu_seqlens (B + 1 offsets, ints or a CPU int32 tensor) with x [H,T,d], g [H,T,d] or [H,T].
     (Up to 255 sequences the offsets travel with the launch.  Of more, a pinned tensor has to stay as it is until the
     call has run, and for every replay of a captured one; captured from other memory they are refused.)
+    stream: a torch stream or a cudaStream_t as an int, None: the current one.  What the call makes itself is made there;
+    the caller orders its inputs before and the use of the results behind it, as with every call that takes a stream.
     Returns (o like x, S_T [B,H,d] float32 or None)."""
     return _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule)[:2]
 
@@ -662,22 +672,22 @@ def efla_scan_backward(x, g, dO, S0=None, dS_T=None, saved=None, cu_seqlens=None
     px, pg = _tensor(x, "x", x.dtype, dev, x.shape), _tensor(g, "g", f32, dev, g.shape)
     pS0, pdO = _tensor(S0, "S0", f32, dev, (B, H, d)), _tensor(dO, "dO", x.dtype, dev, x.shape)
     pdS_T = _tensor(dS_T, "dS_T", f32, dev, (B, H, d))
-    if grads is None:
-        grads = (torch.empty_like(x, dtype=f32), torch.empty_like(g),
-                 x.new_empty((B, H, d), dtype=f32) if want_dS0 else None)
-        out = [None if t is None else t.data_ptr() for t in grads]
-        _made_here(stream, *grads)
-    else:
-        out = [_tensor(t, name, f32, dev, shape)
-               for t, name, shape in zip(grads, ("dx", "dg", "dS0"), (x.shape, g.shape, (B, H, d)))]
-    if workspace is None:
-        n = lib.efla_scan_backward_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None), int(saved is not None))
-        if n == 0:
-            raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_backward_workspace_bytes")
-        workspace = x.new_empty(n, dtype=torch.uint8)
-        _made_here(stream, workspace)
-    else:
-        n = workspace.numel()
+    with _made_on(stream, dev):
+        if grads is None:
+            grads = (torch.empty_like(x, dtype=f32), torch.empty_like(g),
+                     x.new_empty((B, H, d), dtype=f32) if want_dS0 else None)
+            made = grads
+        else:
+            made = ()
+        if workspace is None:
+            n = lib.efla_scan_backward_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None), int(saved is not None))
+            if n == 0:
+                raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_backward_workspace_bytes")
+            workspace = x.new_empty(n, dtype=torch.uint8)
+    _handed_over(stream, dev, *made)
+    out = [_tensor(t, name, f32, dev, shape)
+           for t, name, shape in zip(grads, ("dx", "dg", "dS0"), (x.shape, g.shape, (B, H, d)))]
+    n = workspace.numel()
     ns = 0 if saved is None else saved.numel()
     _call(lib.efla_scan_backward, "efla_scan_backward", dev, stream, px, pg, None if cu is None else cu.data_ptr(), pS0,
           pdO, pdS_T, *out, B, H, T, d, gw, dt, int(rule), _tensor(saved, "saved", torch.uint8, dev, (ns,)), ns,
@@ -704,8 +714,9 @@ def efla_scan_step(x, g, S, o=None, stream=None, rule: int = EFLA_RULE_EXACT) ->
     N, H, d, gw, dt = _step_shape(x, g)
     dev = x.device
     if o is None:
-        o = torch.empty_like(x)
-        _made_here(stream, o)
+        with _made_on(stream, dev):
+            o = torch.empty_like(x)
+        _handed_over(stream, dev, o)
     _call(lib.efla_scan_step, "efla_scan_step", dev, stream, _tensor(x, "x", x.dtype, dev, x.shape),
           _tensor(g, "g", torch.float32, dev, g.shape), _tensor(S, "S", torch.float32, dev, x.shape),
           _tensor(o, "o", x.dtype, dev, x.shape), N, H, d, gw, dt, int(rule))
@@ -744,8 +755,12 @@ def new_pages(n_pages: int, n_slots: int, device="cuda", stream=None) -> EflaPag
     n = int(lib.efla_pages_bytes(n_pages, n_slots))
     if n == 0:
         raise EflaError(EFLA_ERR_INVALID_ARG, "efla_pages_bytes")
-    pages = EflaPages(torch.empty(n // 4, dtype=torch.int32, device=device), n_pages, n_slots)
-    _made_here(stream, pages.block)
+    device = torch.device(device)
+    if device.index is None and device.type == "cuda":
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _made_on(stream, device):
+        pages = EflaPages(torch.empty(n // 4, dtype=torch.int32, device=device), n_pages, n_slots)
+    _handed_over(stream, device, pages.block)
     _call(lib.efla_pages_init, "efla_pages_init", pages.block.device, stream, pages.block.data_ptr(), n, n_pages,
           n_slots)
     return pages
