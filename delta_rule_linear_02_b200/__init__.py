@@ -627,7 +627,8 @@ def _scan_fwd(x, g, S0, cu_seqlens, o, S_T, workspace, want_state, stream, rule)
             n = lib.efla_scan_workspace_bytes(B, H, T, d, gw, dt, int(cu is not None))
             if n == 0:
                 raise EflaError(EFLA_ERR_UNSUPPORTED, "efla_scan_workspace_bytes")
-            workspace = x.new_empty(n, dtype=torch.uint8)
+            # (a call without streams uses no workspace, so its status is that of zeros)
+            workspace = x.new_empty(n, dtype=torch.uint8) if B * H else x.new_zeros(n, dtype=torch.uint8)
             made.append(workspace)
     _handed_over(stream, dev, *made)
     po, pS_T = _tensor(o, "o", x.dtype, dev, x.shape), _tensor(S_T, "S_T", f32, dev, (B, H, d))

@@ -111,7 +111,8 @@ int efla_scan_fwd(const void* x, const float* g, const int* cu_seqlens, const fl
     if (!disjoint(outs, 2, ins, 3) || overlaps(outs[0], outs[2]) || overlaps(outs[1], outs[2]) ||
         overlaps(outs[2], ins[0]) || overlaps(outs[2], ins[1]) || (S_T != S0 && overlaps(outs[2], ins[2])))
         return EFLA_ERR_INVALID_ARG;
-    if (T == 0) {   // no token: the states pass through
+    if (T == 0) {   // no token: the states pass through, and nothing can go wrong on the device
+        if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return EFLA_ERR_CUDA;
         if (!S_T || S_T == S0) return EFLA_OK;
         return from_cuda(S0 ? cudaMemcpyAsync(S_T, S0, ns, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(S_T, 0, ns, s));
     }
@@ -161,6 +162,7 @@ int efla_scan_backward(const void* x, const float* g, const int* cu_seqlens, con
     const Buf outs[4] = {{dx, n * sizeof(float)}, {dg, ng}, {dS0, ns}, {workspace, workspace_bytes}};
     if (!disjoint(outs, 4, ins, 6)) return EFLA_ERR_INVALID_ARG;
     if (T == 0) {
+        if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return EFLA_ERR_CUDA;
         if (!dS0) return EFLA_OK;
         return from_cuda(dS_T ? cudaMemcpyAsync(dS0, dS_T, ns, cudaMemcpyDeviceToDevice, s)
                               : cudaMemsetAsync(dS0, 0, ns, s));

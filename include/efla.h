@@ -427,8 +427,9 @@ int efla_backward_saved(const void *q, const void *k, const void *v, const void 
  *
  * efla_scan_workspace_bytes -- workspace of efla_scan_fwd (packed != 0: with cu_seqlens), 0 for
  * arguments it would reject.  It needs no preparation.  Its first bytes hold the device error word
- * of the last call that used it (a wait that ran out; read it with efla_workspace_status).  Calls
- * that overlap on the GPU must not share a workspace.
+ * of the last call that used it (a wait that ran out; read it with efla_workspace_status); a call
+ * with B = 0 or H = 0 uses none and touches nothing.  Calls that overlap on the GPU must not share
+ * a workspace.
  *
  * efla_scan_fwd -- the forward.  S0 NULL: zero states.  S_T may be NULL (not wanted) or alias S0;
  * otherwise no output may overlap an input, the workspace or another output.  All pointers
