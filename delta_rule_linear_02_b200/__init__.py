@@ -3,13 +3,14 @@
 Argument checks and marshalling only: every step of the computation runs in the library's CUDA
 kernels.  PyTorch provides device memory and streams.  The names mirror the C ABI of
 include/efla.h.  Importing this package loads the in-tree libefla.so and fails loudly if
-it has not been built (python delta_rule_linear_02_b200/build.py).
+it has not been built (python delta_rule_linear_02_b200/build.py); without _efla_native.so it warns.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import os
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -36,16 +37,34 @@ class EflaError(RuntimeError):
         super().__init__(f"{where}: {efla_status_string(status)} ({status})")
 
 
-_native = None      # the short way of the calls whose time is the call itself (csrc/efla_native.cpp)
+class _PythonWay:
+    """In the place of a native module that cannot be used: no call is ordinary, the layer below makes them all."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_native():
+    """The short way of the calls whose time is the call itself (csrc/efla_native.cpp).  Without it, or with one that was
+    built for another torch, the same calls take 5 to 10 us more."""
+    try:
+        from . import _efla_native as native
+        if native.torch_version != torch.__version__:
+            raise ImportError(f"it was built for torch {native.torch_version}, this is {torch.__version__}")
+        return native
+    except ImportError as e:
+        warnings.warn(f"_efla_native.so is not used, calls take longer ({e}); run "
+                      "`python delta_rule_linear_02_b200/build.py`", RuntimeWarning, stacklevel=3)
+        return _PythonWay()
+
+
+_native = _load_native()
 
 
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
-    global _native
     if not os.path.exists(path):
         raise ImportError(f"{os.path.basename(path)} is not built at {path}; run "
                           "`python delta_rule_linear_02_b200/build.py` (nvcc, sm_100a)")
-    if _native is None:
-        from . import _efla_native as _native
     lib = ctypes.CDLL(path)
     vp, I, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_size_t
     lib.efla_status_string.argtypes = [I]

@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -35,15 +36,26 @@ def _stale(out: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _native_stale(mark: str, deps) -> bool:
+    """Whether the binding's native part is missing, older than its sources, or built against another torch or Python."""
+    if not os.path.exists(LIB_NATIVE) or os.path.getmtime(LIB_NATIVE) < max(map(os.path.getmtime, deps)):
+        return True
+    with open(LIB_NATIVE, "rb") as f:
+        return f"efla native: {mark}\0".encode() not in f.read()
+
+
 def build_native(force: bool = False, verbose: bool = False) -> str:
     source = os.path.join(CSRC, "efla_native.cpp")
     deps = [source, os.path.join(INCLUDE, "efla.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(LIB_NATIVE) and os.path.getmtime(LIB_NATIVE) >= max(map(os.path.getmtime, deps)):
-        return LIB_NATIVE
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    version = runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
+    mark = f"torch {version}, {sysconfig.get_config_var('SOABI')}"
+    if not force and not _native_stale(mark, deps):
+        return LIB_NATIVE
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = LIB_NATIVE + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-DNDEBUG", "-I", INCLUDE,
+           f'-DEFLA_BUILT_FOR="{mark}"', f'-DEFLA_TORCH_VERSION="{version}"',
            *(f"-I{d}" for d in (os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
                                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"))),
            "-o", tmp, source, f"-L{os.path.join(torch, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]

@@ -492,4 +492,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_efla_native", nullptr, -1, kMeth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__efla_native() { return PyModule_Create(&kModule); }
+// EFLA_BUILT_FOR: the torch and the Python that this was built against, given by the build, which looks for the mark to
+// see whether it still holds; the Python layer compares the version before it makes a call.
+extern "C" __attribute__((used, visibility("default"))) const char efla_native_mark[] = "efla native: " EFLA_BUILT_FOR;
+
+PyMODINIT_FUNC PyInit__efla_native() {
+    PyObject* m = PyModule_Create(&kModule);
+    if (m && PyModule_AddStringConstant(m, "torch_version", EFLA_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}
