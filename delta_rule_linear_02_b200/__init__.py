@@ -49,8 +49,9 @@ def _load_native():
     built for another torch, the same calls take 5 to 10 us more."""
     try:
         from . import _efla_native as native
-        if native.torch_version != torch.__version__:
-            raise ImportError(f"it was built for torch {native.torch_version}, this is {torch.__version__}")
+        built_for = getattr(native, "torch_version", "unknown")
+        if built_for != torch.__version__:
+            raise ImportError(f"it was built for torch {built_for}, this is {torch.__version__}")
         return native
     except ImportError as e:
         warnings.warn(f"_efla_native.so is not used, calls take longer ({e}); run "

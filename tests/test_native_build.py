@@ -51,10 +51,12 @@ def test_import_without_the_native_part(package):
     assert "build.py" in run()
 
 
-def test_import_with_one_for_another_torch(package):
+@pytest.mark.parametrize("version", ["0.1", "unknown"])
+def test_import_with_one_for_another_torch(package, version):
     to, run = package
-    (to / "_efla_native.py").write_text("torch_version = '0.1'\ndef bind(*a):\n    raise SystemExit('it was called')\n")
-    assert "built for torch 0.1" in run()
+    named = f"torch_version = '{version}'\n" if version != "unknown" else ""
+    (to / "_efla_native.py").write_text(named + "def bind(*a):\n    raise SystemExit('it was called')\n")
+    assert f"built for torch {version}" in run()
 
 
 def test_import_with_the_one_that_was_built(package):
