@@ -598,6 +598,20 @@ def _tensor(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optio
     raise ValueError(f"{name} must be contiguous")
 
 
+def _offsets(cu_seqlens) -> torch.Tensor:
+    """A packed batch's offsets as a contiguous int32 tensor in host memory (one that is that already: itself)."""
+    cu = torch.as_tensor(cu_seqlens, device="cpu")
+    if cu.dim() != 1 or cu.numel() < 2:
+        raise ValueError("cu_seqlens must hold B + 1 offsets of at least one sequence")
+    if cu.is_floating_point() or cu.is_complex() or cu.dtype == torch.bool:
+        raise ValueError(f"cu_seqlens must hold whole numbers, got {cu.dtype}")
+    if cu.dtype != torch.int32:
+        if int(cu.min()) < 0 or int(cu.max()) >= 2 ** 31:
+            raise ValueError("cu_seqlens must hold offsets of 32 bits")
+        cu = cu.to(torch.int32)
+    return cu.contiguous()
+
+
 def _scan_shape(x: torch.Tensor, g: torch.Tensor, cu_seqlens):
     """(B, H, T, d, g_width, dtype, offsets or None) of a dense [B,H,T,d] or packed [H,T,d] batch."""
     if x.dtype not in _DTYPES:
@@ -611,10 +625,8 @@ def _scan_shape(x: torch.Tensor, g: torch.Tensor, cu_seqlens):
         if x.dim() != 3:
             raise ValueError(f"x must be [H,T,d] with cu_seqlens, got {tuple(x.shape)}")
         H, T, d = x.shape
-        cu = torch.as_tensor(cu_seqlens, dtype=torch.int32, device="cpu").contiguous()
+        cu = _offsets(cu_seqlens)
         B = cu.numel() - 1
-        if B < 1 or cu.dim() != 1:
-            raise ValueError("cu_seqlens must hold B + 1 offsets of at least one sequence")
     if g.shape != x.shape and g.shape != x.shape[:-1]:
         raise ValueError(f"g must be {tuple(x.shape)} or {tuple(x.shape[:-1])}, got {tuple(g.shape)}")
     return B, H, T, d, (d if g.dim() == x.dim() else 1), _DTYPES[x.dtype], cu
