@@ -13,9 +13,9 @@
 //   3. the compute warps continue their runs from there and write the outputs.
 // Bound by memory where there are strips enough (444 heads of 128, T 2048, bf16: 150 us, 6.2 TB/s, 95%
 // of the measured copy rate), by a turn's latency, about 2 us from its loads to the next state,
-// where there are few (64 heads: 32 us, 4.2 TB/s; 16 heads, T 32768: 123 us, 4.4 TB/s): strips as
-// narrow as 32 channels and clusters along time are there to have more turns in flight.  A turn of 64 heads' 3370
-// cycles: products 1400, fold 200, exchange 410, entering 240, outputs 600, waits 500; with six blocks in a cluster a turn
+// where there are few (64 heads: 32 us, 4.2 TB/s; 16 heads, T 32768: 125 us, 4.3 TB/s, in a graph of calls, 127 to 129 call
+// by call): strips as narrow as 32 channels and clusters along time are there to have more turns in flight.  A turn of 64
+// heads' 3370 cycles: products 1400, fold 200, exchange 410, entering 240, outputs 600, waits 500; with six blocks in a cluster a turn
 // takes about 4900, half of them the exchange, which waits for the slowest block.
 // Inputs are staged some turns ahead and read from memory once; tokens behind the end and
 // channels beside a head are staged as zeros, which change nothing (e^0 = 1, x = 0).  Everything
@@ -354,12 +354,12 @@ __device__ __forceinline__ float2 chain_turn(const Fold& f, int blocks, const Ge
 }
 
 // The same for a forward's strip of 32 channels in a cluster: of its four parts a warp has two and sends them as one, each
-// half of it to every other block (the long document 130.8 -> 123.8 us.  Within one block, and in the backward, whose
-// registers it takes, it costs more than it gives: layer prefill 32.2 -> 34.5).
+// half of it to every other block (the long document in a graph of calls 131.7 -> 125.0 us, packed requests 76.6 -> 73.2.
+// Within one block, and in the backward, whose registers it takes, it costs more than it gives: layer prefill 32.2 -> 34.5).
 // The decays of two parts, 64 tokens, may multiply to more than fp32 holds where those of each do not (growth), and so may
 // what they leave of their inputs.  The state behind such a pair is then not finite, whatever entered it.  All warps of the
 // cluster read all pairs of the strip, so all see it, and the parts follow (as they do where inputs are not finite).  To look
-// for it costs a turn 0.05 us (the long document 122.7 -> 125.0 in a graph of calls); parts sent apart always take 131.7.
+// for it costs a turn 0.05 us (without it 122.7 and 71.7); a document that grows so in every turn takes 175 us.
 struct Parts {
     float2 mine, h;            // the state entering the warp's own pair, and the last one
     bool dead;
@@ -657,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(ScanArgs P, const
 // from the last to the first.  A tile's own states are put together again from the state that
 // the forward kept for it, so no other state is ever stored.  296 heads of 128, T 2048, bf16: 209 us,
 // 5.9 TB/s (90% of the measured copy rate); 64 heads: 60 us, 4.5 TB/s.  Three kinds of gate of four
-// tokens stay in registers from the products to the gradients: 96 of them a thread, two blocks on an SM.
+// tokens stay in registers from the products to the gradients: 96 of them a thread, two blocks on an SM.  Stages of fp32
+// with a decay per channel are twice as large and leave room for one block: 296 heads 310 us, 5.0 TB/s; 64 heads 84 us.
 template <typename Tin, bool kShared>
 struct BwdSmem {
     static constexpr int kX = kValues * sizeof(Tin), kG = kShared ? 0 : kValues * 4;
@@ -917,6 +918,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const Tin* x, const floa
 // The time of a scan, in microseconds as measured on a B200 (tiles of 4096 bf16 values with a decay
 // per channel): a turn takes 1.3, 1.8 and 2.3 with one to three blocks on an SM, and the exchange
 // about 0.2 + 0.13 per block of the cluster; `held` clusters run at once, the others after them.
+// The rule does not know the type.  Of fp32 with a decay per channel two forward blocks fit on an SM, and one
+// backward block: 64 heads of 128, T 2048, take 37 and 84 us, their bytes 30.7 and 51.1 (bf16: 32 and 60, 20.5 and 40.9).
 double scan_cost(long strips, long steps, int groups, int blocks, long held, long sms) {
     const long rounds = (strips + held - 1) / held, turns = (steps + blocks - 1) / blocks;
     const long share = ((strips < held ? strips : held) * blocks + sms - 1) / sms;
@@ -924,12 +927,12 @@ double scan_cost(long strips, long steps, int groups, int blocks, long held, lon
     return (double)(rounds * turns) * (0.75 + 0.53 * (double)share + exchange);
 }
 
-constexpr long kPlaces = 444;      // of forward blocks, three on each of 148 SMs
+constexpr long kPlaces = 444;      // of forward blocks, three on each of 148 SMs (all types but fp32 with a decay per channel)
 bool lies_evenly(long grid, long places) { return 3 * grid <= places || 4 * grid >= 3 * places; }
 
 // The strips' width: the one with the least time at its best number of blocks, on 148 SMs with
 // three blocks each.  (64 heads of 128, T 2048: 37.5 us at width 128 with four blocks, 34 at 32 with
-// one; 16 heads, T 32768: 263 us at 128 with eight, 123 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
+// one; 16 heads, T 32768: 263 us at 128 with eight, 125 at 32 with six; 444 heads: 150 at 128, 160 at 32.)
 Geo scan_geo(long Z, int T, int d) {
     static thread_local struct {
         long Z;

@@ -53,8 +53,10 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // series on [-1, 1] cut after degree 6 (4.7e-8 off at most): w = 1 + g v, a = 1 + g w, and from phi' = (a - w) / g,
 // w' = w - v.  Nothing cancels near 0, and a long memory's a is as good as its rounding.
 // Elsewhere a is 2^(g log2 e), w = (a - 1) / g and w' = (a - w) / g by their definitions
-// (|a - 1| >= 0.63, |a - w| >= 0.26); a's error there, up to (4 + |g|) 2^-24 relative, belongs to a
-// memory of a token or two.  With u = 2^-24: a below 5 u, w below 6 u, w' below 24 u.
+// (|a - 1| >= 0.63, |a - w| >= 0.26).  Relative errors in u = 2^-24, by their roundings and as measured over 4 million
+// values of g in each range: for |g| < 1 a 5 u (4.9), w 6 u (2.6), w' 24 u (10.5).  Elsewhere a (2.8 + 1.25 |g|) u, from
+// the power's 2^-22.5 and its rounded argument (|g| < 2: 3.5, 8: 8.2, 80: 62.7); for g <= -1 that belongs to a memory of a
+// token or two, and w stays below 6 u (3.4), w' below 24 u (12).  For g >= 1 w and w' have a's error and 3 u.
 // g = -inf gives a = w = w' = 0: the token forgets everything and writes nothing.
 __device__ __forceinline__ void scan_gates1(int rule, float g, float* a, float* w) {
     float v = 2.5358645e-05f;

@@ -5,7 +5,7 @@ u = 2^-24.  A token takes h' to h = a h' + w x.  On the term a h' it adds a's er
 (2.8 + 1.25 |g|) u elsewhere (2^-22.5 of the power, |g| 1.22 u of its rounded argument), a rounding of a product of decays,
 one of the sum that the token is first part of, one of the state that is written, and a third of those of the runs that are
 put together (a run has four tokens; a tile's, a cluster's and a turn's sums follow): 5 + 6 u, beyond |g| = 2 1.25 u more
-per unit of |g|.  On w x: 6 u of w and 5 roundings.  So c = 12 + 1.25 max(|g| - 2, 0) times u for the one and 12 u for
+per unit of |g|.  On w x: 6 u of w (g up to 2) and 5 roundings.  So c = 12 + 1.25 max(|g| - 2, 0) times u for the one and 12 u for
 the other cover both, and the reverse recurrence c' = a (dO + c) alike.
 """
 import torch
